@@ -8,7 +8,7 @@
 namespace kdn {
 
 // Device status word bits (first 32-bit word of the workspace).
-enum : unsigned { kStatusNumeric = 1u, kStatusTimeout = 2u };
+enum : unsigned { kStatusNumeric = 1u, kStatusTimeout = 2u, kStatusInvalid = 4u, kStatusCapacity = 8u };
 
 // Runtime dtype codes, equal to the kdn_dtype values of the public header.
 enum : int { kF32 = 0, kBF16 = 1 };

@@ -252,6 +252,7 @@ const char* kdn_status_string(kdn_status s) {
     case KDN_ERR_CUDA: return "KDN_ERR_CUDA";
     case KDN_ERR_NUMERIC: return "KDN_ERR_NUMERIC";
     case KDN_ERR_TIMEOUT: return "KDN_ERR_TIMEOUT";
+    case KDN_ERR_CAPACITY: return "KDN_ERR_CAPACITY";
   }
   return "KDN_UNKNOWN_STATUS";
 }
@@ -327,7 +328,11 @@ kdn_status kdn_read_device_status(const void* workspace, int* status_out, void* 
   cudaError_t e = cudaMemcpyAsync(&word, word_ptr, sizeof(word), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "reading the device status");
-  *status_out = (word & kdn::kStatusNumeric) ? KDN_ERR_NUMERIC : (word & kdn::kStatusTimeout) ? KDN_ERR_TIMEOUT : KDN_OK;
+  *status_out = (word & kdn::kStatusNumeric)    ? KDN_ERR_NUMERIC
+                : (word & kdn::kStatusTimeout)  ? KDN_ERR_TIMEOUT
+                : (word & kdn::kStatusInvalid)  ? KDN_ERR_INVALID_ARG
+                : (word & kdn::kStatusCapacity) ? KDN_ERR_CAPACITY
+                                                : KDN_OK;
   return ok();
 }
 

@@ -252,6 +252,87 @@ struct SegArgs {
   unsigned* status;
 };
 
+// Causal softmax attention with a sliding window and visible first tokens (n_sink); heads share k and v in groups
+// of H / Hkv.  [B, H, L, d] and [B, Hkv, L, d], head-major like the scans.
+struct WindowArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int in_dtype;
+  int out_dtype;        // of o and dO
+  const int* lens;      // [B] tokens per sequence, or nullptr (L)
+  int B, H, Hkv, L;
+  int window;           // >= 1
+  int n_sink;           // >= 0
+  float scale;
+  void* o;              // forward: out; backward: in
+  float* lse;           // [B, H, L] natural-log normaliser; forward: out; backward: in
+  unsigned* status;
+  // backward
+  const void* dO;
+  float* delta;         // [B, H, L] scratch: dO . o per token
+  void* dq;             // in_dtype
+  void* dk;
+  void* dv;
+  float* part;          // scratch: partial dk, dv of the sink tiles (tensor-core path), or nullptr
+};
+cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& args, cudaStream_t stream);
+cudaError_t launch_window_delta(int dv, const WindowArgs& args, cudaStream_t stream);
+cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& args, cudaStream_t stream);
+
+// The books of a paged key-value cache.
+struct PagesArgs {
+  int num_pages, page_size, rows, max_pages;
+  int* table;           // [rows, max_pages] page numbers, -1 behind a row's pages
+  int* lens;            // [rows] tokens
+  int* refs;            // [num_pages] table entries that name the page
+  unsigned* status;
+  int* scratch;         // pages_scratch_ints(num_pages)
+};
+// The newest ``tokens`` (or counts[i]) tokens of the listed rows.
+struct PagesWrite {
+  int n, heads, tokens;
+  int k_row, v_row;     // bytes of one head's key / value
+  const int* rows;
+  const int* counts;    // or nullptr
+  const void* k_new;    // [n, heads, tokens, dk]
+  const void* v_new;
+  void* k_pages;        // [num_pages, heads, page_size, dk]
+  void* v_pages;
+};
+int pages_max_rows();
+size_t pages_scratch_ints(int num_pages);
+cudaError_t launch_pages_reserve(const PagesArgs& p, int n, const int* rows, const int* counts, int count, cudaStream_t st);
+cudaError_t launch_pages_fork(const PagesArgs& p, int n, const int* src, const int* dst, int* moves, cudaStream_t st);
+cudaError_t launch_pages_free(const PagesArgs& p, int n, const int* rows, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagesArgs& p, int* moves, cudaStream_t st);
+cudaError_t launch_pages_copy(const int* moves, int n, int num_pages, size_t k_bytes, size_t v_bytes, void* k, void* v,
+                              cudaStream_t st);
+cudaError_t launch_pages_write(const PagesArgs& p, const PagesWrite& w, cudaStream_t st);
+
+// One new token per sequence against its paged cache.
+struct PagedStepArgs {
+  const void* q;        // [n, H, dk]
+  const void* k_pages;  // [num_pages, Hkv, page_size, dk]
+  const void* v_pages;
+  int in_dtype, out_dtype;
+  int n, H, Hkv;
+  int num_pages, page_size, rows, max_pages;
+  const int* table;
+  const int* lens;
+  const int* row;       // [n] table row of every sequence, or nullptr (its own index)
+  int window;           // 0 = the whole cache
+  int n_sink;
+  float scale;
+  void* o;              // [n, H, dv]
+  float* lse;           // [n, H] or nullptr
+  int splits;           // parts of a sequence's visible tokens (paged_step_splits)
+  float* part;          // splits > 1: per (sequence, head, split) o [dv], then the maxima and the sums
+};
+int paged_step_splits(int dk, int dv, int in_dtype, int n, int H, int Hkv, long long most_tokens);
+size_t paged_step_part_floats(int dv, int n, int H, int splits);
+cudaError_t launch_paged_step(int dk, int dv, const PagedStepArgs& p, cudaStream_t stream);
+
 cudaError_t launch_seg_uncertainty(int dk, const SegArgs& args, int BH, cudaStream_t stream);
 cudaError_t launch_seg_init(int d, const SegArgs& args, int BH, cudaStream_t stream);
 cudaError_t launch_seg_combine(int d, const SegArgs& args, int BH, cudaStream_t stream);

@@ -16,9 +16,11 @@ for P segments (P must divide L).  Results agree up to rounding.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
+from dataclasses import dataclass
 
 import torch
 
@@ -28,6 +30,7 @@ LIB_PATH = os.path.join(PKG, "lib", "libkdn.so")
 HEADER = os.path.join(ROOT, "include", "kdn.h")
 
 KDN_OK, KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED, KDN_ERR_CUDA, KDN_ERR_NUMERIC, KDN_ERR_TIMEOUT = range(6)
+KDN_ERR_CAPACITY = 6
 KDN_F32, KDN_BF16 = 0, 1
 VARIANTS = {"delta": 0, "kalman_diag": 1, "kalman_full": 2, "kalman_iso": 3}
 _DTYPES = {torch.float32: KDN_F32, torch.bfloat16: KDN_BF16}
@@ -43,6 +46,12 @@ class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int), ("dk", ctypes.c_int),
                 ("dv", ctypes.c_int), ("chunk", ctypes.c_int), ("in_dtype", ctypes.c_int),
                 ("out_dtype", ctypes.c_int), ("segments", ctypes.c_int)]
+
+
+class PagesC(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("rows", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
 
 
 _lib = None
@@ -97,6 +106,21 @@ def lib() -> ctypes.CDLL:
     L.kdn_plan.argtypes = [i, dims, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_char_p),
                            ctypes.POINTER(ctypes.c_char_p)]
     L.kdn_plan.restype = ctypes.c_int
+    pages = ctypes.POINTER(PagesC)
+    L.kdn_window_attn.argtypes = [dims, i, vp, vp, vp, vp, i, i, f, vp, vp, vp, sz, vp]
+    L.kdn_window_attn_backward.argtypes = [dims, i, vp, vp, vp, vp, i, i, f] + [vp] * 7 + [sz, vp]
+    L.kdn_window_workspace_bytes.argtypes = [dims, i, i, i]
+    L.kdn_pages_reserve.argtypes = [pages, i, vp, vp, i, vp, sz, vp]
+    L.kdn_pages_fork.argtypes = [pages, i, vp, vp, vp, vp, sz, vp]
+    L.kdn_pages_free.argtypes = [pages, i, vp, vp, sz, vp]
+    L.kdn_pages_compact.argtypes = [pages, vp, vp, sz, vp]
+    L.kdn_pages_workspace_bytes.argtypes = [pages]
+    L.kdn_pages_copy.argtypes = [i, vp, i, i, i, i, i, i, vp, vp, vp]
+    L.kdn_pages_write.argtypes = [pages, i, vp, vp, i, i, i, i, i, vp, vp, vp, vp, vp]
+    L.kdn_paged_attn_step.argtypes = [pages, i, vp, i, i, i, i, i, i, vp, vp, vp, i, i, f, vp, vp, vp, sz, vp]
+    L.kdn_paged_step_workspace_bytes.argtypes = [pages] + [i] * 8
+    for name in ("kdn_window_workspace_bytes", "kdn_pages_workspace_bytes", "kdn_paged_step_workspace_bytes"):
+        getattr(L, name).restype = sz
     for name in ("kdn_scan_delta", "kdn_scan_kalman_full", "kdn_scan_kalman_diag", "kdn_decode_step",
                  "kdn_read_device_status"):
         getattr(L, name).restype = ctypes.c_int
@@ -470,3 +494,281 @@ def selftest_wait_timeout(workspace: torch.Tensor | None, wait_cycles: int = 100
     nothing in flight): afterwards ``read_device_status(workspace)`` reports KDN_ERR_TIMEOUT."""
     st = lib().kdn_selftest_wait_timeout(_ptr(workspace), int(wait_cycles), _stream(stream))
     _check(st, "kdn_selftest_wait_timeout")
+
+
+# ---------------------------------------------------------------------------------- windowed attention
+
+def _on(stream):
+    """Allocations of a call belong to the stream it runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _stream_of(stream, dev):
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace
+
+
+def _window_args(q, k, v, lens, scale):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, H, L, d_k], k [B, kv_heads, L, d_k] and v [B, kv_heads, L, d_v]")
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported input dtype {q.dtype}")
+    B, H, L, dk = q.shape
+    Hkv, dv = k.shape[1], v.shape[-1]
+    dev = q.device
+    _need(q, "q", (B, H, L, dk), q.dtype)
+    _need(k, "k", (B, Hkv, L, dk), q.dtype, dev)
+    _need(v, "v", (B, Hkv, L, dv), q.dtype, dev)
+    if lens is not None:
+        _need(lens, "lens", (B,), torch.int32, dev)
+    return B, H, Hkv, L, dk, dv, dev, float(dk ** -0.5 if scale is None else scale)
+
+
+def window_workspace_bytes(B, H, Hkv, L, dk, dv, n_sink=0, in_dtype=torch.bfloat16, out_dtype=None, backward=False):
+    d = Dims(B, H, L, dk, dv, 0, _DTYPES[in_dtype], _DTYPES[out_dtype or in_dtype], 0)
+    return int(lib().kdn_window_workspace_bytes(ctypes.byref(d), Hkv, n_sink, int(backward)))
+
+
+def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=None, workspace=None, out_dtype=None,
+                stream=None):
+    """Causal softmax attention in which token t sees the tokens j <= t with j > t - window or j < n_sink.
+
+    q [B,H,L,d_k], k [B,kv_heads,L,d_k], v [B,kv_heads,L,d_v] (bf16 or fp32); query head h reads k/v head
+    h // (H / kv_heads).  lens [B] int32 (or None): tokens of each sequence; rows behind them are left as they were
+    in the given o and lse, and are zero in those allocated here.  scale defaults to 1 / sqrt(d_k), out_dtype to q's.
+    Returns (o [B,H,L,d_v], lse [B,H,L] fp32)."""
+    B, H, Hkv, L, dk, dv, dev, scale = _window_args(q, k, v, lens, scale)
+    out_dtype = out_dtype or (q.dtype if o is None else o.dtype)
+    if out_dtype not in _DTYPES:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    dims = Dims(B, H, L, dk, dv, 0, _DTYPES[q.dtype], _DTYPES[out_dtype], 0)
+    new = torch.empty if lens is None else torch.zeros
+    with _on(stream):
+        if o is None:
+            o = new(B, H, L, dv, dtype=out_dtype, device=dev)
+        if lse is None:
+            lse = new(B, H, L, dtype=torch.float32, device=dev)
+        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, n_sink, 0), dev)
+    _need(o, "o", (B, H, L, dv), out_dtype, dev)
+    _need(lse, "lse", (B, H, L), torch.float32, dev)
+    st = lib().kdn_window_attn(ctypes.byref(dims), Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(lens), window, n_sink, scale,
+                               _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_window_attn")
+    return o, lse
+
+
+def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale=None, dq=None, dk=None, dv=None,
+                         workspace=None, stream=None):
+    """Gradients of window_attn for upstream dO (of o's type), from its inputs and its o and lse.  Returns a dict with
+    dq, dk, dv in q's type (dk and dv summed over the heads that share them); rows behind a sequence's last token are
+    left as they were in given tensors, and are zero in those allocated here."""
+    B, H, Hkv, L, d_k, d_v, dev, scale = _window_args(q, k, v, lens, scale)
+    if o.dtype not in _DTYPES:
+        raise ValueError(f"unsupported output dtype {o.dtype}")
+    _need(o, "o", (B, H, L, d_v), o.dtype, dev)
+    _need(lse, "lse", (B, H, L), torch.float32, dev)
+    _need(dO, "dO", (B, H, L, d_v), o.dtype, dev)
+    dims = Dims(B, H, L, d_k, d_v, 0, _DTYPES[q.dtype], _DTYPES[o.dtype], 0)
+    new = torch.empty if lens is None else torch.zeros
+    with _on(stream):
+        dq = new(B, H, L, d_k, dtype=q.dtype, device=dev) if dq is None else dq
+        dk = new(B, Hkv, L, d_k, dtype=q.dtype, device=dev) if dk is None else dk
+        dv = new(B, Hkv, L, d_v, dtype=q.dtype, device=dev) if dv is None else dv
+        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, n_sink, 1), dev)
+    _need(dq, "dq", (B, H, L, d_k), q.dtype, dev)
+    _need(dk, "dk", (B, Hkv, L, d_k), q.dtype, dev)
+    _need(dv, "dv", (B, Hkv, L, d_v), q.dtype, dev)
+    st = lib().kdn_window_attn_backward(ctypes.byref(dims), Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(lens), window, n_sink,
+                                        scale, _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv),
+                                        _ptr(workspace), workspace.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_window_attn_backward")
+    return {"dq": dq, "dk": dk, "dv": dv}
+
+
+# ---------------------------------------------------------------------------------- paged key-value cache
+
+@dataclass
+class Pages:
+    """The books of a paged cache (kdn_pages): table [rows, max_pages], lens [rows] and refs [num_pages], int32.  One
+    set serves every layer; a layer's pages are k_pages [num_pages, kv_heads, page_size, d_k] and v_pages.
+    ``workspace`` (allocated at the first call) holds the status of the last book-keeping call:
+    read_device_status(pages.workspace)."""
+    table: torch.Tensor
+    lens: torch.Tensor
+    refs: torch.Tensor
+    page_size: int
+    workspace: torch.Tensor | None = None
+
+    def _c(self, dev=None):
+        if self.table.dim() != 2:
+            raise ValueError("table must be [rows, max_pages]")
+        rows, most = self.table.shape
+        _need(self.table, "table", (rows, most), torch.int32, dev)
+        dev = self.table.device
+        _need(self.lens, "lens", (rows,), torch.int32, dev)
+        _need(self.refs, "refs", (self.refs.numel(),), torch.int32, dev)
+        return PagesC(self.refs.numel(), self.page_size, rows, most, self.table.data_ptr(), self.lens.data_ptr(),
+                      self.refs.data_ptr())
+
+
+def make_pages(num_pages, page_size, rows, max_pages, device="cuda") -> Pages:
+    """The books of an empty cache."""
+    full = lambda shape, x: torch.full(shape, x, dtype=torch.int32, device=device)  # noqa: E731
+    return Pages(full((rows, max_pages), -1), full((rows,), 0), full((num_pages,), 0), page_size)
+
+
+def _list(t, name, dev):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D int32 tensor")
+    return _need(t, name, (t.shape[0],), torch.int32, dev)
+
+
+def _books(pages, stream):
+    c = pages._c()
+    dev = pages.table.device
+    if pages.workspace is None:
+        with _on(stream):
+            pages.workspace = _scratch(None, lib().kdn_pages_workspace_bytes(ctypes.byref(c)), dev)
+    return c, dev, pages.workspace
+
+
+def pages_reserve(pages, rows, counts, stream=None):
+    """Adds tokens to the listed rows (int32 [n]), with the pages they need: ``counts`` each, or counts[i] (int32 [n])."""
+    c, dev, ws = _books(pages, stream)
+    _list(rows, "rows", dev)
+    each = isinstance(counts, torch.Tensor)
+    if each:
+        _need(counts, "counts", rows.shape, torch.int32, dev)
+    st = lib().kdn_pages_reserve(ctypes.byref(c), rows.numel(), _ptr(rows), _ptr(counts) if each else None,
+                                 0 if each else counts, _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_pages_reserve")
+
+
+def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
+    """Makes each empty row dst_rows[i] a copy of src_rows[i], sharing its full pages.  Returns moves [n, 2] int32, the
+    part-filled pages that pages_copy has to copy (in every layer) before the rows are used."""
+    c, dev, ws = _books(pages, stream)
+    _list(src_rows, "src_rows", dev)
+    _need(dst_rows, "dst_rows", src_rows.shape, torch.int32, dev)
+    with _on(stream):
+        if moves is None:
+            moves = torch.empty(src_rows.numel(), 2, dtype=torch.int32, device=dev)
+    _need(moves, "moves", (src_rows.numel(), 2), torch.int32, dev)
+    st = lib().kdn_pages_fork(ctypes.byref(c), src_rows.numel(), _ptr(src_rows), _ptr(dst_rows), _ptr(moves), _ptr(ws),
+                              ws.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_pages_fork")
+    return moves
+
+
+def pages_free(pages, rows, stream=None):
+    """Empties the listed rows; pages that no row names any more are free."""
+    c, dev, ws = _books(pages, stream)
+    _list(rows, "rows", dev)
+    st = lib().kdn_pages_free(ctypes.byref(c), rows.numel(), _ptr(rows), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_pages_free")
+
+
+def pages_compact(pages, moves=None, stream=None):
+    """Moves the pages in use to the lowest page numbers.  Returns moves [num_pages // 2, 2] int32 for pages_copy (in
+    every layer), ending in pairs of -1."""
+    c, dev, ws = _books(pages, stream)
+    with _on(stream):
+        if moves is None:
+            moves = torch.empty(c.num_pages // 2, 2, dtype=torch.int32, device=dev)
+    _need(moves, "moves", (c.num_pages // 2, 2), torch.int32, dev)
+    st = lib().kdn_pages_compact(ctypes.byref(c), _ptr(moves), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_pages_compact")
+    return moves
+
+
+def _pool(k_pages, v_pages, dev=None):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, kv_heads, page_size, d_k] and v_pages [num_pages, kv_heads, page_size, d_v]")
+    if k_pages.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {k_pages.dtype} of k_pages")
+    num, Hkv, page, dk = k_pages.shape
+    dv = v_pages.shape[-1]
+    _need(k_pages, "k_pages", (num, Hkv, page, dk), k_pages.dtype, dev)
+    _need(v_pages, "v_pages", (num, Hkv, page, dv), k_pages.dtype, k_pages.device)
+    return num, Hkv, page, dk, dv
+
+
+def pages_copy(moves, k_pages, v_pages, stream=None):
+    """Copies page moves[i, 0] to page moves[i, 1] for every pair (pairs with a number out of range are skipped)."""
+    num, Hkv, page, dk, dv = _pool(k_pages, v_pages)
+    dev = k_pages.device
+    _need(moves, "moves", (moves.shape[0], 2), torch.int32, dev)
+    st = lib().kdn_pages_copy(moves.shape[0], _ptr(moves), num, page, Hkv, dk, dv, _DTYPES[k_pages.dtype], _ptr(k_pages),
+                              _ptr(v_pages), _stream_of(stream, dev))
+    _check(st, "kdn_pages_copy")
+
+
+def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream=None):
+    """Writes the newest tokens of the listed rows (added by pages_reserve) into one layer's pages: k_new
+    [n, kv_heads, tokens, d_k] and v_new; of entry i the first counts[i] (or all) are the row's last counts[i]."""
+    dev = pages.table.device
+    num, Hkv, page, dk, dv = _pool(k_pages, v_pages, dev)
+    c = pages._c()
+    if num != c.num_pages or page != pages.page_size:
+        raise ValueError(f"k_pages holds {num} pages of {page} tokens, the books {c.num_pages} of {pages.page_size}")
+    _list(rows, "rows", dev)
+    n = rows.numel()
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [n, kv_heads, tokens, d_k]")
+    T = k_new.shape[2]
+    _need(k_new, "k_new", (n, Hkv, T, dk), k_pages.dtype, dev)
+    _need(v_new, "v_new", (n, Hkv, T, dv), k_pages.dtype, dev)
+    if counts is not None:
+        _need(counts, "counts", (n,), torch.int32, dev)
+    st = lib().kdn_pages_write(ctypes.byref(c), n, _ptr(rows), _ptr(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype],
+                               _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _stream_of(stream, dev))
+    _check(st, "kdn_pages_write")
+
+
+def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sink=0, scale=None, o=None, lse=None,
+                    workspace=None, out_dtype=None, stream=None):
+    """One new token per sequence against its paged cache, which already holds it (pages_write): q [n,H,d_k], sequence i
+    being row rows[i] (int32 [n]; None: i) of table [rows, max_pages] and lens [rows].  window = 0 sees the whole
+    cache; otherwise visibility is window_attn's.  Returns (o [n,H,d_v], lse [n,H] fp32); an empty row gives 0 and
+    -inf, a broken table entry NaN."""
+    num, Hkv, page, dk, dv = _pool(k_pages, v_pages)
+    dev = k_pages.device
+    if q.dim() != 3:
+        raise ValueError("q must be [n, H, d_k]")
+    n, H = q.shape[:2]
+    _need(q, "q", (n, H, dk), k_pages.dtype, dev)
+    if table.dim() != 2:
+        raise ValueError("table must be [rows, max_pages]")
+    _need(table, "table", tuple(table.shape), torch.int32, dev)
+    _need(lens, "lens", (table.shape[0],), torch.int32, dev)
+    if rows is not None:
+        _need(rows, "rows", (n,), torch.int32, dev)
+    out_dtype = out_dtype or (q.dtype if o is None else o.dtype)
+    if out_dtype not in _DTYPES:
+        raise ValueError(f"unsupported output dtype {out_dtype}")
+    c = PagesC(num, page, table.shape[0], table.shape[1], table.data_ptr(), lens.data_ptr(), None)
+    with _on(stream):
+        if o is None:
+            o = torch.empty(n, H, dv, dtype=out_dtype, device=dev)
+        if lse is None:
+            lse = torch.empty(n, H, dtype=torch.float32, device=dev)
+        need = lib().kdn_paged_step_workspace_bytes(ctypes.byref(c), n, H, Hkv, dk, dv, _DTYPES[q.dtype], window, n_sink)
+        workspace = _scratch(workspace, need, dev)
+    _need(o, "o", (n, H, dv), out_dtype, dev)
+    _need(lse, "lse", (n, H), torch.float32, dev)
+    scale = float(dk ** -0.5 if scale is None else scale)
+    st = lib().kdn_paged_attn_step(ctypes.byref(c), n, _ptr(rows), H, Hkv, dk, dv, _DTYPES[q.dtype], _DTYPES[out_dtype],
+                                   _ptr(q), _ptr(k_pages), _ptr(v_pages), window, n_sink, scale, _ptr(o), _ptr(lse),
+                                   _ptr(workspace), workspace.numel(), _stream_of(stream, dev))
+    _check(st, "kdn_paged_attn_step")
+    return o, lse

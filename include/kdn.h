@@ -86,7 +86,8 @@ typedef enum kdn_status {
   KDN_ERR_UNSUPPORTED = 2,  /* valid request outside the supported sizes */
   KDN_ERR_CUDA = 3,         /* a CUDA runtime call or launch failed */
   KDN_ERR_NUMERIC = 4,      /* device status: non-positive / non-finite innovation variance */
-  KDN_ERR_TIMEOUT = 5       /* device status: a bounded wait gave up */
+  KDN_ERR_TIMEOUT = 5,      /* device status: a bounded wait gave up */
+  KDN_ERR_CAPACITY = 6      /* device status: a paged cache has no page, or a row no entry, left */
 } kdn_status;
 
 typedef enum kdn_dtype { KDN_F32 = 0, KDN_BF16 = 1 } kdn_dtype;
@@ -281,6 +282,112 @@ KDN_EXPORT kdn_status kdn_hola_cache_read(const kdn_dims* dims, const void* q, c
  * the status word, plus B*H*ceil(L/64)*64 int32 cache indices where the
  * tensor-core path applies); 0 for invalid dims.  Pure host call. */
 KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
+
+/* Causal softmax attention with a sliding window and visible first tokens: the recency read that layers of
+ * this kind are mixed with (A Hippocampus for Linear Attention, section 3.4, takes the same softmax read over
+ * a surprise cache and the tokens of one block).  Token t of a sequence sees
+ *   vis(t) = { j <= t : j > t - window or j < n_sink },
+ *   lse_t = log sum_{j in vis(t)} exp(scale q_t . k_j),  o_t = sum_{j in vis(t)} exp(scale q_t . k_j - lse_t) v_j.
+ * q [B,H,L,d_k], k [B,kv_heads,L,d_k], v [B,kv_heads,L,d_v] (dims->in_dtype): query head h reads k/v head
+ * h / (H / kv_heads); kv_heads divides H.  lens [B] int32 or NULL (= L): tokens of each sequence, held to
+ * [0, L]; what memory holds behind a sequence's last token takes no part (it may be NaN), and its rows of o
+ * and lse are left as they were.  window >= 1 (>= L: plain causal attention), n_sink >= 0, scale > 0.
+ * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
+ * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
+ * enter the second product as bf16; sums, maxima and both products' accumulators are fp32), everything else
+ * on the fp32 cores.  workspace: kdn_window_workspace_bytes(dims, kv_heads, n_sink, 0) bytes.  Asynchronous. */
+KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
+                           const int* lens, int window, int n_sink, float scale, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of kdn_window_attn: from the forward's inputs, its o and lse and the upstream dO [B,H,L,d_v]
+ * (dims->out_dtype, as o), the gradients dq [B,H,L,d_k], dk [B,kv_heads,L,d_k], dv [B,kv_heads,L,d_v], in
+ * dims->in_dtype (accumulated in fp32, rounded once; dk and dv summed over the heads that share them).  With
+ * delta_t = dO_t . o_t, P_tj = exp(scale q_t . k_j - lse_t) and dS_tj = P_tj (dO_t . v_j - delta_t):
+ *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
+ * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
+ * gradients do not change from run to run.  Rows behind a sequence's last token are left as they were; lse has
+ * no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, n_sink, 1) bytes. */
+KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
+                                    const void* v, const int* lens, int window, int n_sink, float scale,
+                                    const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of kdn_window_attn (backward = 0) or kdn_window_attn_backward (1); 0 for invalid dims. */
+KDN_EXPORT size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int n_sink, int backward);
+
+/* The books of a paged key-value cache.  Keys and values of all sequences lie in pages of page_size tokens,
+ *   k_pages [num_pages, kv_heads, page_size, d_k],  v_pages [num_pages, kv_heads, page_size, d_v]  (16-byte aligned),
+ * and row r of the table lists the pages of one sequence: token j of row r is token j % page_size of page
+ * table[r][j / page_size].  One set of books serves any number of layers (each with pages of its own).
+ *   table [rows, max_pages] int32: page numbers, -1 behind a row's ceil(lens[r] / page_size) pages
+ *   lens  [rows] int32: tokens of each row (0 = empty)
+ *   refs  [num_pages] int32: table entries that name the page (0 = free)
+ * All three are device arrays of the caller's; an empty cache is table = -1, lens = 0, refs = 0.
+ * page_size: a power of two up to 1024.  At most 262,144 rows and 2^30 tokens per row. */
+typedef struct kdn_pages {
+  int num_pages, page_size, rows, max_pages;
+  int* table;
+  int* lens;
+  int* refs;
+} kdn_pages;
+
+/* Book-keeping calls.  Each is carried out as a whole or, when it cannot be, changes nothing and sets the status
+ * word (kdn_read_device_status): KDN_ERR_INVALID_ARG for a row out of range or listed twice, KDN_ERR_CAPACITY
+ * when no page or no table entry is left.  New pages are the lowest free ones, in the order of the list.  rows
+ * are device arrays of n int32.  workspace: kdn_pages_workspace_bytes(pages) bytes; asynchronous; the calls on
+ * one cache must be ordered (one stream, or events).
+ *   reserve  adds counts[i] (counts NULL: count) tokens to row rows[i], with the pages they need; a row may be
+ *            listed once.  The tokens themselves are written with kdn_pages_write.
+ *   fork     makes the empty row dst_rows[i] a copy of src_rows[i]: full pages are shared, a part-filled last page
+ *            gets a page of its own, and moves[i] = (old page, new page), or (-1, -1), says what kdn_pages_copy has
+ *            to copy before either row is written or read again.  A source may be listed often; a destination once,
+ *            and not as a source.
+ *   free     empties the rows (listed twice: freed once); pages that no row names any more are free.
+ *   compact  moves the pages in use into the lowest page numbers: the i-th used page behind them goes into the i-th
+ *            free one among them.  moves [num_pages / 2][2] int32: the (old, new) pairs, then (-1, -1); every layer
+ *            has to be copied with kdn_pages_copy before the cache is used again. */
+KDN_EXPORT kdn_status kdn_pages_reserve(const kdn_pages* pages, int n, const int* rows, const int* counts, int count,
+                             void* workspace, size_t workspace_bytes, void* stream);
+KDN_EXPORT kdn_status kdn_pages_fork(const kdn_pages* pages, int n, const int* src_rows, const int* dst_rows, int* moves,
+                          void* workspace, size_t workspace_bytes, void* stream);
+KDN_EXPORT kdn_status kdn_pages_free(const kdn_pages* pages, int n, const int* rows, void* workspace,
+                          size_t workspace_bytes, void* stream);
+KDN_EXPORT kdn_status kdn_pages_compact(const kdn_pages* pages, int* moves, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of workspace of the book-keeping calls; 0 for invalid sizes. */
+KDN_EXPORT size_t kdn_pages_workspace_bytes(const kdn_pages* pages);
+
+/* Copies page moves[i][0] to page moves[i][1] (keys and values of one layer) for the n pairs; pairs with a
+ * number outside [0, num_pages) are skipped.  No destination may be another pair's source or destination. */
+KDN_EXPORT kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int page_size, int kv_heads, int dk, int dv,
+                          kdn_dtype dtype, void* k_pages, void* v_pages, void* stream);
+
+/* Writes the newest tokens of rows rows[0..n) into one layer's pages, after kdn_pages_reserve has added them:
+ * k_new [n, kv_heads, tokens, d_k], v_new [n, kv_heads, tokens, d_v]; of entry i the first counts[i] (NULL: tokens)
+ * are the last counts[i] tokens of the row.  Entries whose row, count or page is out of range are skipped. */
+KDN_EXPORT kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens,
+                           int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new,
+                           void* k_pages, void* v_pages, void* stream);
+
+/* One new token per sequence against the paged cache, next to kdn_decode_step's against the resident state.
+ * Sequence i is row rows[i] (rows NULL: i) of the table, its new token the row's last, already written.
+ *   q [n, H, d_k] (in_dtype, as the pages), o [n, H, d_v] (out_dtype), lse [n, H] fp32 or NULL;
+ * visibility as in kdn_window_attn for t = lens - 1, window = 0 meaning the whole cache.  An empty row gives o = 0
+ * and lse = -inf.  A row or a visible table entry outside its range is not followed: that sequence's o and lse are
+ * NaN.  Long caches are split over the GPU's SMs and the parts joined in a fixed order.  H / kv_heads query heads
+ * share a k/v head and read it once.  bf16 pages with d_k = d_v in {64, 128} run on the tensor cores with the
+ * softmax weights as bf16 hi + lo pairs.  workspace: kdn_paged_step_workspace_bytes(...) bytes (only scratch: the
+ * call has no device status). */
+KDN_EXPORT kdn_status kdn_paged_attn_step(const kdn_pages* pages, int n, const int* rows, int H, int kv_heads, int dk,
+                               int dv, kdn_dtype in_dtype, kdn_dtype out_dtype, const void* q, const void* k_pages,
+                               const void* v_pages, int window, int n_sink, float scale, void* o, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of kdn_paged_attn_step; 0 for invalid sizes.  Pure host call: it reads none of the arrays. */
+KDN_EXPORT size_t kdn_paged_step_workspace_bytes(const kdn_pages* pages, int n, int H, int kv_heads, int dk, int dv,
+                                      kdn_dtype in_dtype, int window, int n_sink);
 
 /* kdn_scan_kalman_full for callers that cannot allocate device memory.  The
  * pages have no counterpart: this is a deployment variant.  Callers that must

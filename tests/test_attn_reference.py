@@ -1,0 +1,157 @@
+"""The references of the windowed attention against each other, against differences, and the library's host-side
+refusals (no GPU)."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.attn as oa
+from attn_ref import dense
+from delta_rule_recurrent_scan_b200 import build, kdn
+
+
+def _draw(B, H, Hkv, L, dk, dv, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(B, h, L, d, generator=g, dtype=torch.float64) for h, d in ((H, dk), (Hkv, dk), (Hkv, dv), (H, dv))]
+
+
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (4, 0), (4, 2), (3, 9), (100, 3)])
+def test_dense_reference_is_the_row_by_row_oracle(window, n_sink):
+    q, k, v, dO = _draw(2, 4, 2, 13, 8, 6)
+    lens = torch.tensor([13, 5], dtype=torch.int32)
+    d = dense(q, k, v, window, n_sink, lens, dO=dO, out=0.0)
+    o, lse = oa.window_attn(q, k, v, window, n_sink, lens)
+    g = oa.window_attn_backward(q, k, v, dO, window, n_sink, lens)
+    for name, x in (("o", o), ("lse", lse), ("dq", g["dq"]), ("dk", g["dk"]), ("dv", g["dv"])):
+        np.testing.assert_allclose(d[name][0].numpy(), x, rtol=1e-10, atol=1e-12)
+
+
+def test_gradients_against_differences():
+    q, k, v, dO = (x.numpy() for x in _draw(1, 2, 1, 7, 4, 3, seed=1))
+    g = oa.window_attn_backward(q, k, v, dO, 3, 1)
+    loss = lambda: float((oa.window_attn(q, k, v, 3, 1)[0] * dO).sum())  # noqa: E731
+    for x, name in ((q, "dq"), (k, "dk"), (v, "dv")):
+        for at in np.ndindex(*x.shape):
+            keep = x[at]
+            x[at] = keep + 1e-5
+            hi = loss()
+            x[at] = keep - 1e-5
+            lo = loss()
+            x[at] = keep
+            assert abs((hi - lo) / 2e-5 - g[name][at]) < 1e-7
+
+
+def test_paged_step_oracle_is_the_last_row_of_the_window():
+    q, k, v, _ = _draw(1, 4, 2, 21, 8, 8, seed=2)
+    o, lse = oa.window_attn(q, k, v, 6, 3)
+    kp, vp = (torch.zeros(6, 2, 4, 8, dtype=torch.float64) for _ in range(2))
+    table = [[3, 1, 5, 0, 2, 4]]
+    for t in range(21):
+        kp[table[0][t // 4], :, t % 4], vp[table[0][t // 4], :, t % 4] = k[0, :, t], v[0, :, t]
+    o1, lse1 = oa.paged_attn_step(q[:, :, -1], kp, vp, table, [21], window=6, n_sink=3)
+    np.testing.assert_allclose(o1, o[:, :, -1], rtol=1e-12)
+    np.testing.assert_allclose(lse1, lse[:, :, -1], rtol=1e-12)
+
+
+# ------------------------------------------------------------------------------------------ refusals
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return kdn.lib()
+
+
+def _attn(L, d, kv=1, window=4, n_sink=0, scale=1.0):
+    return L.kdn_window_attn(ctypes.byref(d), kv, None, None, None, None, window, n_sink, scale, None, None, None, 0, None)
+
+
+def test_window_attention_refusals(L):
+    d = kdn.Dims(1, 4, 8, 64, 64, 0, 1, 1, 0)
+    assert _attn(L, d, kv=3) == kdn.KDN_ERR_INVALID_ARG and b"kv_heads" in L.kdn_last_error()
+    assert _attn(L, d, kv=0) == kdn.KDN_ERR_INVALID_ARG
+    assert _attn(L, d, window=0) == kdn.KDN_ERR_INVALID_ARG and b"window" in L.kdn_last_error()
+    assert _attn(L, d, n_sink=-1) == kdn.KDN_ERR_INVALID_ARG
+    for bad in (0.0, -1.0, float("inf"), float("nan")):
+        assert _attn(L, d, scale=bad) == kdn.KDN_ERR_INVALID_ARG and b"scale" in L.kdn_last_error()
+    assert _attn(L, kdn.Dims(1, 4, 8, 48, 64, 0, 1, 1, 0)) == kdn.KDN_ERR_UNSUPPORTED
+    assert _attn(L, kdn.Dims(1 << 14, 1 << 10, 1 << 14, 64, 64, 0, 1, 1, 0)) == kdn.KDN_ERR_UNSUPPORTED
+    assert _attn(L, d) == kdn.KDN_ERR_INVALID_ARG and b"q is NULL" in L.kdn_last_error()
+    args = [None] * 3 + [None, 4, 0, 1.0] + [None] * 7 + [0, None]
+    assert L.kdn_window_attn_backward(ctypes.byref(d), 1, *args) == kdn.KDN_ERR_INVALID_ARG
+    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 3, 0, 1) == 0
+    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 0, 0) >= 256
+    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 0, 1) >= 256 + 4 * 8 * 4
+
+
+def test_paged_cache_refusals(L):
+    ok = dict(num_pages=8, page_size=16, rows=4, max_pages=2)
+    assert L.kdn_pages_workspace_bytes(ctypes.byref(kdn.PagesC(**ok))) >= 256 + 4 * 16
+    for bad, status in ((dict(num_pages=0), 1), (dict(rows=0), 1), (dict(max_pages=0), 1), (dict(page_size=0), 2),
+                        (dict(page_size=24), 2), (dict(page_size=2048), 2), (dict(rows=1 << 20), 2),
+                        (dict(max_pages=1 << 30), 2)):
+        c = kdn.PagesC(**{**ok, **bad})
+        assert L.kdn_pages_workspace_bytes(ctypes.byref(c)) == 0
+        assert L.kdn_pages_free(ctypes.byref(c), 0, None, None, 0, None) == status
+        assert L.kdn_paged_step_workspace_bytes(ctypes.byref(c), 1, 4, 2, 64, 64, 1, 0, 0) == 0
+    c = kdn.PagesC(**ok)
+    assert L.kdn_pages_free(None, 0, None, None, 0, None) == kdn.KDN_ERR_INVALID_ARG
+    assert L.kdn_pages_free(ctypes.byref(c), -1, None, None, 0, None) == kdn.KDN_ERR_INVALID_ARG
+    assert L.kdn_pages_reserve(ctypes.byref(c), 1, None, None, -1, None, 0, None) == kdn.KDN_ERR_INVALID_ARG
+    assert L.kdn_pages_free(ctypes.byref(c), 0, None, None, 0, None) == kdn.KDN_ERR_INVALID_ARG
+    assert b"table" in L.kdn_last_error()
+    step = lambda n=1, H=4, kv=2, dk=64, dv=64, it=1, ot=1, window=0, sink=0, scale=1.0: L.kdn_paged_attn_step(  # noqa: E731
+        ctypes.byref(c), n, None, H, kv, dk, dv, it, ot, None, None, None, window, sink, scale, None, None, None, 0, None)
+    assert step(kv=3) == kdn.KDN_ERR_INVALID_ARG
+    assert step(dk=48) == kdn.KDN_ERR_UNSUPPORTED
+    assert step(it=7) == kdn.KDN_ERR_INVALID_ARG and step(ot=7) == kdn.KDN_ERR_INVALID_ARG
+    assert step(window=-1) == kdn.KDN_ERR_INVALID_ARG and step(sink=-1) == kdn.KDN_ERR_INVALID_ARG
+    assert step(scale=0.0) == kdn.KDN_ERR_INVALID_ARG
+    assert step(n=5) == kdn.KDN_ERR_INVALID_ARG and b"rows" in L.kdn_last_error()
+    assert step(n=-1) == kdn.KDN_ERR_INVALID_ARG
+    assert L.kdn_pages_copy(1, None, 8, 16, 2, 64, 64, 1, None, None, None) == kdn.KDN_ERR_INVALID_ARG
+    assert L.kdn_pages_copy(1, None, 8, 24, 2, 64, 64, 1, None, None, None) == kdn.KDN_ERR_UNSUPPORTED
+    assert L.kdn_status_string(6).decode() == "KDN_ERR_CAPACITY"
+
+
+def test_binding_refuses_cpu_tensors_and_bad_shapes():
+    x = torch.zeros(1, 2, 4, 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        kdn.window_attn(x, x, x, 4)
+    with pytest.raises(ValueError, match="q must be"):
+        kdn.window_attn(x[0], x, x, 4)
+    with pytest.raises(ValueError, match="unsupported"):
+        kdn.window_attn(x.half(), x, x, 4)
+    pages = kdn.make_pages(4, 16, 2, 2, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        kdn.pages_free(pages, torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        kdn.paged_attn_step(x[0], x, x, pages.table, pages.lens)
+
+
+def test_books_oracle_keeps_its_counts():
+    """refs always equals the number of table entries naming a page, through a run of every call."""
+    b = oa.Books(12, 4, 5, 4)
+
+    def count():
+        n = [0] * 12
+        for r, row in enumerate(b.table):
+            held = [p for p in row if p >= 0]
+            assert len(held) == -(-b.lens[r] // 4)
+            for p in held:
+                n[p] += 1
+        assert n == b.refs
+
+    assert b.reserve([0, 2], [9, 4]) == "ok"
+    count()
+    assert b.table[0][:3] == [0, 1, 2] and b.table[2][0] == 3
+    assert b.fork([0, 0, 2], [1, 3, 4]) == ("ok", [(2, 4), (2, 5), (-1, -1)])
+    count()
+    assert b.refs[0] == 3 and b.fork([0], [1])[0] == "invalid"
+    assert b.free([0, 0]) == "ok"
+    count()
+    assert b.reserve([1], [8]) == "capacity" and b.reserve([1, 1], [1, 1]) == "invalid"
+    assert b.reserve([2], [40]) == "capacity"
+    assert b.compact()[0] == (5, 2)
+    count()
