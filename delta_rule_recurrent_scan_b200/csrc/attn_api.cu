@@ -135,7 +135,8 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
   if (none) return ok();
   kdn::WindowArgs a{};
   a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens;
-  a.B = dims->B, a.H = dims->H, a.Hkv = kv_heads, a.L = dims->L, a.window = window, a.n_sink = n_sink, a.scale = scale;
+  a.B = dims->B, a.H = dims->H, a.Hkv = kv_heads, a.L = dims->L, a.scale = scale;
+  a.window = window < dims->L ? window : dims->L, a.n_sink = n_sink < dims->L ? n_sink : dims->L;  // t - j < L
   a.o = o, a.lse = lse, a.status = static_cast<unsigned*>(workspace);
   return cuda_status(kdn::launch_window_attn(dims->dk, dims->dv, a, st), "windowed attention launch");
 }
@@ -163,7 +164,8 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
   if (none) return clear_status(workspace, st);
   kdn::WindowArgs a{};
   a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens;
-  a.B = dims->B, a.H = dims->H, a.Hkv = kv_heads, a.L = dims->L, a.window = window, a.n_sink = n_sink, a.scale = scale;
+  a.B = dims->B, a.H = dims->H, a.Hkv = kv_heads, a.L = dims->L, a.scale = scale;
+  a.window = window < dims->L ? window : dims->L, a.n_sink = n_sink < dims->L ? n_sink : dims->L;  // t - j < L
   a.o = const_cast<void*>(o), a.lse = const_cast<float*>(lse), a.status = static_cast<unsigned*>(workspace);
   a.dO = dO, a.dq = dq, a.dk = dk, a.dv = dv;
   a.delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);

@@ -31,6 +31,8 @@ struct ChunkArgs {
 
 // [BH][L][d] bf16 viewed as a 3-D tensor map with 64 x 64 boxes and the 128-byte swizzle.
 bool make_bf16_tmap(CUtensorMap* tm, const void* base, int BH, int L, int d);
+// The same view with boxes of ``rows`` x 64.
+bool make_bf16_tmap_rows(CUtensorMap* tm, const void* base, int BH, int L, int d, int rows);
 
 // Covariance side of the full-Kalman scan, chunked (Woodbury / LDL): per-token gains into ``gains``
 // ([BH, L, d] fp32) and P updated in place.  d in {64, 128}, bf16 keys.

@@ -30,13 +30,13 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [BH][L][d] bf16 viewed as a 3-D tensor; 64 x 64 boxes with the 128-byte swizzle.
-bool make_tmap_impl(CUtensorMap* tm, const void* base, int BH, int L, int d) {
+// [BH][L][d] bf16 viewed as a 3-D tensor; boxes of rows x 64 with the 128-byte swizzle.
+bool make_tmap_impl(CUtensorMap* tm, const void* base, int BH, int L, int d, int rows) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)BH};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)L * d * 2};
-  cuuint32_t box[3] = {64, 64, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -45,7 +45,11 @@ bool make_tmap_impl(CUtensorMap* tm, const void* base, int BH, int L, int d) {
 
 }  // namespace
 
-bool make_bf16_tmap(CUtensorMap* tm, const void* base, int BH, int L, int d) { return make_tmap_impl(tm, base, BH, L, d); }
+bool make_bf16_tmap(CUtensorMap* tm, const void* base, int BH, int L, int d) { return make_tmap_impl(tm, base, BH, L, d, 64); }
+
+bool make_bf16_tmap_rows(CUtensorMap* tm, const void* base, int BH, int L, int d, int rows) {
+  return make_tmap_impl(tm, base, BH, L, d, rows);
+}
 
 bool chunk_supported(kdn_variant variant, const kdn_dims& d) {
   (void)variant;

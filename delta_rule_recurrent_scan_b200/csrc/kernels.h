@@ -277,6 +277,9 @@ struct WindowArgs {
   float* part;          // scratch: partial dk, dv of the sink tiles (tensor-core path), or nullptr
 };
 cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& args, cudaStream_t stream);
+// tensor-core variant (bf16, d_k = d_v = 64 or 128); launch_window_attn picks it when it applies
+bool window_tc_supported(int dk, int dv, int in_dtype);
+cudaError_t launch_window_attn_tc(int d, const WindowArgs& args, cudaStream_t stream);
 cudaError_t launch_window_delta(int dv, const WindowArgs& args, cudaStream_t stream);
 cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& args, cudaStream_t stream);
 

@@ -398,6 +398,7 @@ cudaError_t for_dim(int d, F f) {
 }  // namespace
 
 cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& p, cudaStream_t stream) {
+  if (window_tc_supported(dk, dv, p.in_dtype)) return launch_window_attn_tc(dk, p, stream);
   return for_dim(dk, [&](auto k) { return for_dim(dv, [&](auto v) { return forward<k(), v()>(p, stream); }); });
 }
 
