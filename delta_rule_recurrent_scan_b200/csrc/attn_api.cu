@@ -109,10 +109,14 @@ size_t elem_bytes(kdn_dtype t) { return t == KDN_BF16 ? 2 : 4; }
 
 extern "C" {
 
-size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int n_sink, int backward) {
-  if (check_dims(dims) != KDN_OK || check_heads(dims->H, kv_heads) != KDN_OK || n_sink < 0) return 0;
+size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int window, int n_sink, int backward) {
+  if (check_dims(dims) != KDN_OK || check_heads(dims->H, kv_heads) != KDN_OK || window < 1 || n_sink < 0) return 0;
   size_t n = kStatusBytes;
-  if (backward) n += round256((size_t)dims->B * dims->H * (size_t)dims->L * sizeof(float));
+  if (!backward || dims->L == 0) return n;
+  if (kdn::window_tc_supported(dims->dk, dims->dv, dims->in_dtype))
+    n += round256(kdn::window_bwd_tc_scratch_bytes(dims->B, dims->H, kv_heads, dims->L, dims->dk, dims->out_dtype, window, n_sink));
+  else
+    n += round256((size_t)dims->B * dims->H * (size_t)dims->L * sizeof(float));
   return n;
 }
 
@@ -127,7 +131,7 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
   KDN_TRY(check_ptr(o, "o", 16, none));
   KDN_TRY(check_ptr(lse, "lse", 4, none));
   KDN_TRY(check_ptr(lens, "lens", 4, true));
-  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_window_workspace_bytes(dims, kv_heads, n_sink, 0)));
+  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 0)));
   DeviceGuard guard;
   KDN_TRY(use_device_of(workspace, guard));
   cudaStream_t st = (cudaStream_t)stream;
@@ -157,7 +161,7 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
   KDN_TRY(check_ptr(dk, "dk", 16, none));
   KDN_TRY(check_ptr(dv, "dv", 16, none));
   KDN_TRY(check_ptr(lens, "lens", 4, true));
-  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_window_workspace_bytes(dims, kv_heads, n_sink, 1)));
+  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1)));
   DeviceGuard guard;
   KDN_TRY(use_device_of(workspace, guard));
   cudaStream_t st = (cudaStream_t)stream;
@@ -168,7 +172,8 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
   a.window = window < dims->L ? window : dims->L, a.n_sink = n_sink < dims->L ? n_sink : dims->L;  // t - j < L
   a.o = const_cast<void*>(o), a.lse = const_cast<float*>(lse), a.status = static_cast<unsigned*>(workspace);
   a.dO = dO, a.dq = dq, a.dk = dk, a.dv = dv;
-  a.delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+  a.scratch = static_cast<char*>(workspace) + kStatusBytes;
+  a.delta = static_cast<float*>(a.scratch);
   return cuda_status(kdn::launch_window_attn_backward(dims->dk, dims->dv, a, st), "windowed attention backward launch");
 }
 

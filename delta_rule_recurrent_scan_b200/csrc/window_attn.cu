@@ -402,14 +402,11 @@ cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& p, cudaStream_t
   return for_dim(dk, [&](auto k) { return for_dim(dv, [&](auto v) { return forward<k(), v()>(p, stream); }); });
 }
 
-cudaError_t launch_window_delta(int dv, const WindowArgs& p, cudaStream_t stream) {
+cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& p, cudaStream_t stream) {
+  if (window_tc_supported(dk, dv, p.in_dtype)) return launch_window_bwd_tc(dk, p, stream);
   const size_t rows = (size_t)p.B * p.H * p.L;
   window_delta_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p, dv);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& p, cudaStream_t stream) {
-  const cudaError_t e = launch_window_delta(dv, p, stream);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return for_dim(dk, [&](auto k) { return for_dim(dv, [&](auto v) { return backward<k(), v()>(p, stream); }); });
 }

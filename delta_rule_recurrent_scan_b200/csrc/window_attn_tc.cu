@@ -19,36 +19,15 @@
 //
 // v rows behind a sequence's end are set to zero in shared memory (0 times whatever memory holds there would not be 0);
 // k rows behind it only reach hidden scores.
-#include <cuda.h>
-
-#include "chunk.h"
-#include "chunk_common.cuh"
-#include "sm100.cuh"
-#include "window.cuh"
+#include "window_tc.cuh"
 
 namespace kdn {
 
 namespace {
 
-using chunk::kWaitCycles;
-using window::KeyTiles;
+using namespace window;
 
-constexpr int kT = 128;              // queries and keys per tile
-constexpr int kPanel = kT * 128;     // bytes of a swizzled panel: 128 rows of 64 bf16
-constexpr int kThreads = 320;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // growth of the maximum (base 2) that weights may keep
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 template <int D>
 struct Smem {
@@ -57,7 +36,7 @@ struct Smem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, WindowArgs p) {
   using S = Smem<D>;
@@ -124,24 +103,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = b * p.Hkv + kvh;
       sm100::mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * S::kTile);
       for (int i = 0; i < (two ? 2 : 1); ++i)
-#pragma unroll
-        for (int pn = 0; pn < kNP; ++pn)
-          sm100::tma_load_3d(sm + S::kQ + i * S::kTile + pn * kPanel, &tm_q, &q_full, 64 * pn, qt[i] * kT, b * p.H + h[i]);
+        load_tile<kNP>(sm + S::kQ + i * S::kTile, &tm_q, &q_full, qt[i] * kT, b * p.H + h[i]);
       int it = 0;
       for (; it < n; ++it) {
         const int slot = it & 1, round = it >> 1, j0 = ku.walk(it) * kT;
         if (round > 0) fine = sm100::mbar_wait_bounded(&k_empty[slot], (round - 1) & 1, kWaitCycles);
         if (!fine) break;
         sm100::mbar_arrive_expect_tx(&k_full[slot], S::kTile);
-#pragma unroll
-        for (int pn = 0; pn < kNP; ++pn)
-          sm100::tma_load_3d(sm + S::kK + slot * S::kTile + pn * kPanel, &tm_k, &k_full[slot], 64 * pn, j0, row);
+        load_tile<kNP>(sm + S::kK + slot * S::kTile, &tm_k, &k_full[slot], j0, row);
         if (round > 0) fine = sm100::mbar_wait_bounded(&v_empty[slot], (round - 1) & 1, kWaitCycles);
         if (!fine) break;
         sm100::mbar_arrive_expect_tx(&v_full[slot], S::kTile);
-#pragma unroll
-        for (int pn = 0; pn < kNP; ++pn)
-          sm100::tma_load_3d(sm + S::kV + slot * S::kTile + pn * kPanel, &tm_v, &v_full[slot], 64 * pn, j0, row);
+        load_tile<kNP>(sm + S::kV + slot * S::kTile, &tm_v, &v_full[slot], j0, row);
       }
       if (!fine) {  // nothing of this CTA may be in flight when it ends
         sm100::mbar_wait_bounded(&q_full, 0, kWaitCycles);
@@ -153,24 +126,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------------------ products
-    constexpr uint32_t id_s = sm100::idesc_bf16(128, kT, false, false);
-    constexpr uint32_t id_o = sm100::idesc_bf16(128, D, false, true);
     const uint32_t q_addr = sm100::smem_u32(sm + S::kQ), k_addr = sm100::smem_u32(sm + S::kK), v_addr = sm100::smem_u32(sm + S::kV);
     auto issue_s = [&](int i, int it) {
       if (lane == 0) {
-        const uint32_t qa = q_addr + i * S::kTile, ka = k_addr + (it & 1) * S::kTile;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * kPanel + (ks % 4) * 32;
-          sm100::mma_bf16(tmem + 128 * i, sm100::smem_desc(qa + off, 16, 1024), sm100::smem_desc(ka + off, 16, 1024), id_s, ks > 0);
-        }
+        mma_rows<D>(tmem + 128 * i, q_addr + i * S::kTile, k_addr + (it & 1) * S::kTile);
         sm100::mma_commit(&s_ready[i]);
       }
     };
     uint32_t p_phase[2] = {0, 0};
     bool begun[2] = {false, false};
-    fine = sm100::mbar_wait_bounded(&q_full, 0, kWaitCycles) && sm100::mbar_wait_bounded(&k_full[0], 0, kWaitCycles);
-    fine = __all_sync(0xffffffffu, fine);
+    fine = warp_wait(&q_full, 0) && warp_wait(&k_full[0], 0);
     if (fine) {
       if (active(0, 0)) issue_s(0, 0);
       if (active(1, 0)) issue_s(1, 0);
@@ -178,34 +143,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int it = 0; it < n && fine; ++it) {
       const int slot = it & 1, round = it >> 1, j0 = ku.walk(it) * kT;
-      fine = sm100::mbar_wait_bounded(&v_full[slot], round & 1, kWaitCycles);
-      if (it + 1 < n) fine = fine && sm100::mbar_wait_bounded(&k_full[(it + 1) & 1], ((it + 1) >> 1) & 1, kWaitCycles);
-      fine = __all_sync(0xffffffffu, fine);
+      fine = warp_wait(&v_full[slot], round & 1);
+      if (it + 1 < n) fine = fine && warp_wait(&k_full[(it + 1) & 1], ((it + 1) >> 1) & 1);
       if (!fine) break;
-      if (j0 + kT > len) {  // v rows behind the end: zero, so that a hidden weight times them is zero
-        const int first = len - j0, words = (kT - first) * 8;
-        for (int e = lane; e < words * kNP; e += 32) {
-          const int pn = e / words, w = e % words;
-          *reinterpret_cast<uint4*>(sm + S::kV + slot * S::kTile + pn * kPanel + (first + w / 8) * 128 + (w % 8) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        sm100::fence_async_smem();
-        __syncwarp();
-      }
+      if (j0 + kT > len) zero_rows<kNP>(sm + S::kV + slot * S::kTile, len - j0, lane);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (active(i, it)) {
-          fine = __all_sync(0xffffffffu, sm100::mbar_wait_bounded(&p_ready[i], p_phase[i], kWaitCycles));
+          fine = warp_wait(&p_ready[i], p_phase[i]);
           if (!fine) break;
           p_phase[i] ^= 1;
           sm100::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t va = v_addr + slot * S::kTile;
-#pragma unroll
-            for (int ks = 0; ks < kT / 16; ++ks)
-              sm100::mma_bf16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * ks, sm100::smem_desc(va + ks * 2048, kPanel, 1024), id_o,
-                                 begun[i] || ks > 0);
-          }
+          if (lane == 0) mma_weights<D>(tmem + 256 + D * i, tmem + 128 * i, 32, v_addr + slot * S::kTile, begun[i]);
           begun[i] = true;
         }
         if (it + 1 < n && active(i, it + 1)) issue_s(i, it + 1);
@@ -234,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < n && mine; ++it) {
       if (!active(i, it)) continue;
       const int j0 = ku.walk(it) * kT;
-      fine = __all_sync(0xffffffffu, sm100::mbar_wait_bounded(&s_ready[i], phase, kWaitCycles));
+      fine = warp_wait(&s_ready[i], phase);
       if (!fine) break;
       phase ^= 1;
       sm100::tc_fence_after();
@@ -299,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_arrive(&p_ready[i]);
     }
     if (mine && fine) {
-      fine = __all_sync(0xffffffffu, sm100::mbar_wait_bounded(&done, 0, kWaitCycles));
+      fine = warp_wait(&done, 0);
       sm100::tc_fence_after();
       if (fine) {
         const float inv = 1.f / l;
@@ -314,9 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.out_dtype == kBF16) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + u);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int e = 0; e < 4; ++e) dst[e] = pack8_bf16(o + 8 * e, inv);
           } else {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D + u);
 #pragma unroll
@@ -344,7 +291,7 @@ cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
   const int smem = Smem<D>::kTotal + 1024;
   const cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  window_fwd_tc_kernel<D><<<(unsigned)ctas, kThreads, smem, stream>>>(tq, tk, tv, p);
+  window_fwd_tc_kernel<D><<<(unsigned)ctas, kTcThreads, smem, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,625 @@
+// Backward of the windowed attention on the sm_100a tensor cores: bf16, d_k = d_v = 64 or 128.
+//
+//   P = exp2(S scale log2(e) - lse log2(e)),  dP = dO v^T,  dS = P (dP - delta),  delta = dO . o per query,
+//   dv = P^T dO,  dk = scale dS^T q,  dq = scale dS k.
+//
+// Two passes over the visible tile pairs, each with its accumulators in TMEM for the whole walk: one CTA per 128 keys
+// for dk and dv, one per 128 queries for dq.  Computing S and dP twice (7 products per pair instead of 5) leaves every
+// sum in one CTA in a fixed order: no atomics, no fp32 dq in memory, gradients equal from run to run.  In both passes
+// the weights go from registers to TMEM as the A operand of the next product and never to shared memory:
+//
+//   keys:    S^T = k q^T and dP^T = v dO^T have the key on the TMEM lane, so P^T and dS^T lie as dv += P^T dO and
+//            dk += dS^T q need them.  TMEM: S^T, dP^T (128 columns each), dv, dk (d each); the weights overlay the scores.
+//   queries: S and dP have the query on the lane; dq += dS k.  S is free as soon as it is in registers, so the next
+//            tile's S and dP (two buffers) run while this tile's dS is made.
+//
+// P and dS are rounded to bf16 for their product (the other operand's type; 2^-8 of a weight at most); the sums are fp32.
+// A warpgroup takes half of a tile's columns: thread = (lane, half).  One load warp (TMA rings of two slots), one warp
+// whose first lane issues the products.  Rows behind a sequence's end are zeroed in shared memory.
+//
+// The key tiles that hold sinks are seen by every later query.  Where there are one or two of them their walk is cut
+// into parts of a regular tile's length; the parts' fp32 sums go to the workspace and a last launch adds them in order.
+#include "window_tc.cuh"
+
+namespace kdn {
+
+namespace {
+
+using namespace window;
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = (D / 64) * kPanel;
+  static constexpr int kFixed = 0;                 // the two tiles a CTA keeps
+  static constexpr int kRing = 2 * kTile;          // two slots of the two tiles it walks
+  static constexpr int kTotal = 6 * kTile;
+};
+
+// ------------------------------------------------------------------------------------------ per-query scalars
+// rows[token] = (lse log2(e), delta), and dO as bf16 where it came as fp32.  One warp per token.
+template <int D>
+__global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* rows, __nv_bfloat16* dO16) {
+  const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing of this call has raised it yet
+  if (row >= (size_t)p.B * p.H * p.L) return;
+  const int b = static_cast<int>(row / ((size_t)p.H * p.L)), t = static_cast<int>(row % p.L);
+  if (t >= window::seq_len(p, b)) return;
+  float x = 0.f;
+  constexpr int E = D / 32;  // 2 or 4 elements per lane
+  float o[E], g[E];
+  const size_t at = row * D + E * lane;
+  if (p.out_dtype == kBF16) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.o) + at + e);
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.dO) + at + e);
+      o[e] = __uint_as_float(a << 16), o[e + 1] = __uint_as_float(a & 0xffff0000u);
+      g[e] = __uint_as_float(c << 16), g[e + 1] = __uint_as_float(c & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 a = *reinterpret_cast<const float2*>(static_cast<const float*>(p.o) + at + e);
+      const float2 c = *reinterpret_cast<const float2*>(static_cast<const float*>(p.dO) + at + e);
+      o[e] = a.x, o[e + 1] = a.y, g[e] = c.x, g[e + 1] = c.y;
+      *reinterpret_cast<uint32_t*>(dO16 + at + e) = pack_bf16(c.x, c.y);  // an operand of two bf16 products
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) x = fmaf(o[e], g[e], x);
+  x = warp_sum(x);
+  if (lane == 0) rows[row] = make_float2(p.lse[row] * kLog2e, x);
+}
+
+// ------------------------------------------------------------------------------------------ dk, dv
+struct KeyPass {
+  int sinks;   // key tiles whose walk is cut
+  int parts;   // into this many parts
+  float* part; // [B, Hkv, sinks, parts, 2, 128, D]
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    window_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, WindowArgs p,
+                          const float2* rows, KeyPass kp) {
+  using S = Smem<D>;
+  constexpr int kNP = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(16) float2 rows_s[2][kT];
+  __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], s_ready, p_ready, dp_ready, ds_ready, done;
+  __shared__ uint32_t tmem_base;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
+  // the cut walks come first (they are the longest), then the other key tiles
+  unsigned x = blockIdx.x;
+  const unsigned cut = (unsigned)bh * kp.sinks * kp.parts;
+  int tile, part = 0, y;
+  const bool is_cut = x < cut;
+  if (is_cut) {
+    part = x % kp.parts, x /= kp.parts;
+    tile = x % kp.sinks, y = x / kp.sinks;
+  } else {
+    x -= cut;
+    const int rest = tiles - kp.sinks;
+    tile = kp.sinks + x % rest, y = x / rest;
+  }
+  const int kvh = y % p.Hkv, b = y / p.Hkv;
+  const int len = window::seq_len(p, b), j0 = tile * kT;
+  if (j0 >= len) return;
+  int lo, hi;
+  window::query_tiles<kT>(j0, min(j0 + kT, len) - 1, len, p.window, p.n_sink, lo, hi);
+  const int per = hi - lo, all = per * G;  // (head of the group, query tile), query tiles fastest
+  const int first = is_cut ? (int)((long long)all * part / kp.parts) : 0;
+  const int n = (is_cut ? (int)((long long)all * (part + 1) / kp.parts) : all) - first;
+
+  if (tid == 0) {
+    sm100::mbar_init(&kv_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&q_full[i], 33), sm100::mbar_init(&q_empty[i], 1);  // the copy and 32 lanes' row scalars
+      sm100::mbar_init(&do_full[i], 1), sm100::mbar_init(&do_empty[i], 1);
+    }
+    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&p_ready, 256);
+    sm100::mbar_init(&dp_ready, 1), sm100::mbar_init(&ds_ready, 256);
+    sm100::mbar_init(&done, 1);
+    sm100::fence_mbar_init();
+  }
+  if (warp == 9) {
+    sm100::tmem_alloc(&tmem_base, 512);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+  bool fine = true;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------------------------ loads
+    if (lane == 0 && n > 0) {
+      sm100::prefetch_tmap(&tm_q), sm100::prefetch_tmap(&tm_do);
+      sm100::mbar_arrive_expect_tx(&kv_full, 2 * S::kTile);
+      load_tile<kNP>(sm + S::kFixed, &tm_k, &kv_full, j0, b * p.Hkv + kvh);
+      load_tile<kNP>(sm + S::kFixed + S::kTile, &tm_v, &kv_full, j0, b * p.Hkv + kvh);
+    }
+    int it = 0;
+    bool q_sent = false;
+    for (; it < n; ++it) {
+      const int slot = it & 1, round = it >> 1, item = first + it;
+      const int row = b * p.H + kvh * G + item / per, t0 = (lo + item % per) * kT;
+      q_sent = false;
+      if (round > 0) fine = warp_wait(&q_empty[slot], (round - 1) & 1);
+      if (!fine) break;
+      if (lane == 0) {
+        sm100::mbar_arrive_expect_tx(&q_full[slot], S::kTile);
+        load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_q, &q_full[slot], t0, row);
+      }
+      q_sent = true;
+      // the rows' scalars; behind the end lse = inf makes every weight zero
+#pragma unroll
+      for (int u = 0; u < kT / 32; ++u) {
+        const int r = lane + 32 * u;
+        rows_s[slot][r] = t0 + r < len ? rows[(size_t)row * p.L + t0 + r] : make_float2(INFINITY, 0.f);
+      }
+      sm100::mbar_arrive(&q_full[slot]);
+      if (round > 0) fine = warp_wait(&do_empty[slot], (round - 1) & 1);
+      if (!fine) break;
+      if (lane == 0) {
+        sm100::mbar_arrive_expect_tx(&do_full[slot], S::kTile);
+        load_tile<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, &tm_do, &do_full[slot], t0, row);
+      }
+    }
+    if (!fine) {  // nothing of this CTA may be in flight when it ends
+      sm100::mbar_wait_bounded(&kv_full, 0, kWaitCycles);
+      for (int back = it > 1 ? it - 1 : 0; back <= it && back < n; ++back) {
+        if (back < it || q_sent) sm100::mbar_wait_bounded(&q_full[back & 1], (back >> 1) & 1, kWaitCycles);
+        if (back < it) sm100::mbar_wait_bounded(&do_full[back & 1], (back >> 1) & 1, kWaitCycles);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------------------------ products
+    const uint32_t k_addr = sm100::smem_u32(sm + S::kFixed), v_addr = k_addr + S::kTile;
+    const uint32_t ring = sm100::smem_u32(sm + S::kRing);
+    auto q_of = [&](int it) { return ring + 2 * (it & 1) * S::kTile; };
+    auto do_of = [&](int it) { return ring + (2 * (it & 1) + 1) * S::kTile; };
+    auto end_of = [&](int it) { return len - (lo + (first + it) % per) * kT; };  // rows of this tile inside the sequence
+    auto issue_s = [&](int it) {
+      if (end_of(it) < kT) zero_rows<kNP>(sm + S::kRing + 2 * (it & 1) * S::kTile, end_of(it), lane);
+      if (lane == 0) mma_rows<D>(t_s, k_addr, q_of(it)), sm100::mma_commit(&s_ready);
+    };
+    auto issue_dp = [&](int it) {
+      if (end_of(it) < kT) zero_rows<kNP>(sm + S::kRing + (2 * (it & 1) + 1) * S::kTile, end_of(it), lane);
+      if (lane == 0) mma_rows<D>(t_dp, v_addr, do_of(it)), sm100::mma_commit(&dp_ready);
+    };
+    if (n > 0) {
+      fine = warp_wait(&kv_full, 0) && warp_wait(&q_full[0], 0) && warp_wait(&do_full[0], 0);
+      if (fine) issue_s(0), issue_dp(0);
+    }
+    for (int it = 0; it < n && fine; ++it) {
+      const int slot = it & 1, next = (it + 1) & 1, next_round = (it + 1) >> 1;
+      fine = warp_wait(&p_ready, it & 1);
+      if (!fine) break;
+      sm100::tc_fence_after();
+      if (lane == 0) {
+        mma_weights<D>(t_dv, t_s, 64, do_of(it), it > 0);
+        sm100::mma_commit(&do_empty[slot]);
+      }
+      if (it + 1 < n) {
+        fine = warp_wait(&q_full[next], next_round & 1);
+        if (!fine) break;
+        issue_s(it + 1);
+      }
+      fine = warp_wait(&ds_ready, it & 1);
+      if (!fine) break;
+      sm100::tc_fence_after();
+      if (lane == 0) {
+        mma_weights<D>(t_dk, t_dp, 64, q_of(it), it > 0);
+        sm100::mma_commit(&q_empty[slot]);
+      }
+      if (it + 1 < n) {
+        fine = warp_wait(&do_full[next], next_round & 1);
+        if (!fine) break;
+        issue_dp(it + 1);
+      }
+    }
+    if (lane == 0) {
+      sm100::mma_commit(&done);
+      if (!fine) sm100::mbar_wait_bounded(&done, 0, kWaitCycles);
+    }
+  } else {
+    // ------------------------------------------------------------------------------------ weights
+    const int half = warp >> 2, key = tid & 127, j = j0 + key;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const float c = p.scale * kLog2e;
+    const int j_first = j0 + 32 * (warp & 3), j_last = j_first + 31;
+    const bool sink = j < p.n_sink;
+    for (int it = 0; it < n; ++it) {
+      const int t0 = (lo + (first + it) % per) * kT + 64 * half;  // this half's first query
+      fine = warp_wait(&q_full[it & 1], (it >> 1) & 1) && warp_wait(&s_ready, it & 1);  // the row scalars and S^T
+      if (!fine) break;
+      sm100::tc_fence_after();
+      float s[2][32];
+      sm100::tmem_ld32(t_s + lanes + 64 * half, s[0]);
+      sm100::tmem_ld32(t_s + lanes + 64 * half + 32, s[1]);
+      sm100::tmem_wait_ld();
+      const float4* rs = reinterpret_cast<const float4*>(&rows_s[it & 1][64 * half]);  // two queries a word
+      const bool all_seen = t0 >= j_last && (t0 + 63 - j_first < p.window || j_last < p.n_sink);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float4 r = rs[16 * u + e / 2];
+          s[u][e] = exp2_fast(fmaf(s[u][e], c, -r.x));
+          s[u][e + 1] = exp2_fast(fmaf(s[u][e + 1], c, -r.z));
+        }
+      if (!all_seen) {  // query t sees key j: t >= j and (t < j + window or a sink)
+        const int near = j - t0, far = near + p.window;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = 32 * u + e;
+            if (col < near || (col >= far && !sink)) s[u][e] = 0.f;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(pack_bf16(s[u][2 * e], s[u][2 * e + 1]));
+        sm100::tmem_st16(t_s + lanes + 64 * half + 16 * u, w);
+      }
+      sm100::tmem_wait_st();
+      sm100::tc_fence_before();
+      sm100::mbar_arrive(&p_ready);
+      fine = warp_wait(&dp_ready, it & 1);
+      if (!fine) break;
+      sm100::tc_fence_after();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float dp[32], w[16];
+        sm100::tmem_ld32(t_dp + lanes + 64 * half + 32 * u, dp);
+        sm100::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 r = rs[16 * u + e];
+          w[e] = __uint_as_float(pack_bf16(s[u][2 * e] * (dp[2 * e] - r.y), s[u][2 * e + 1] * (dp[2 * e + 1] - r.w)));
+        }
+        sm100::tmem_st16(t_dp + lanes + 64 * half + 16 * u, w);
+      }
+      sm100::tmem_wait_st();
+      sm100::tc_fence_before();
+      sm100::mbar_arrive(&ds_ready);
+    }
+    if (fine) {
+      fine = warp_wait(&done, 0);
+      sm100::tc_fence_after();
+    }
+    if (fine) {  // half 0 writes dv, half 1 dk
+      const uint32_t t_out = (half == 0 ? t_dv : t_dk) + lanes;
+      const float f = half == 0 ? 1.f : p.scale;
+      const size_t at = ((size_t)(b * p.Hkv + kvh) * p.L + j) * D;
+      float* cut_out = kp.part + ((((size_t)(b * p.Hkv + kvh) * kp.sinks + tile) * kp.parts + part) * 2 + half) * kT * D + key * D;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half == 0 ? p.dv : p.dk) + at;
+#pragma unroll 1
+      for (int u = 0; u < D; u += 32) {
+        float a[32];
+        sm100::tmem_ld32(t_out + u, a);
+        sm100::tmem_wait_ld();
+        if (n == 0) {  // a part without a tile: nothing was added
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = 0.f;
+        }
+        if (is_cut) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(cut_out + u + 4 * e) = make_float4(a[4 * e] * f, a[4 * e + 1] * f, a[4 * e + 2] * f, a[4 * e + 3] * f);
+        } else if (j < len) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(out + u + 8 * e) = pack8_bf16(a + 8 * e, f);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (!fine) raise_status(p.status, kStatusTimeout);
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) sm100::tmem_dealloc(tmem, 512);
+}
+
+// The cut tiles' parts, added in their order; a thread has 8 consecutive values.
+template <int D>
+__global__ void __launch_bounds__(256) window_join_kernel(WindowArgs p, KeyPass kp) {
+  constexpr int kWords = 2 * kT * D / 8;
+  const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t which = e / kWords;  // (sequence, k/v head, tile)
+  if (which >= (size_t)p.B * p.Hkv * kp.sinks) return;
+  const int w = static_cast<int>(e % kWords), half = w / (kT * D / 8), key = w / (D / 8) % kT, c = w % (D / 8) * 8;
+  const int tile = static_cast<int>(which % kp.sinks);
+  const size_t head = which / kp.sinks;
+  const int j = tile * kT + key;
+  if (j >= window::seq_len(p, static_cast<int>(head / p.Hkv))) return;
+  const float* from = kp.part + which * kp.parts * 2 * kT * D + (half * kT + key) * D + c;
+  float a[8] = {};
+  for (int i = 0; i < kp.parts; ++i) {
+    const float4 u = *reinterpret_cast<const float4*>(from + (size_t)i * 2 * kT * D);
+    const float4 v = *reinterpret_cast<const float4*>(from + (size_t)i * 2 * kT * D + 4);
+    a[0] += u.x, a[1] += u.y, a[2] += u.z, a[3] += u.w, a[4] += v.x, a[5] += v.y, a[6] += v.z, a[7] += v.w;
+  }
+  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(half == 0 ? p.dv : p.dk) + (head * p.L + j) * D + c) = pack8_bf16(a, 1.f);
+}
+
+// ------------------------------------------------------------------------------------------ dq
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    window_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, WindowArgs p,
+                        const float2* rows) {
+  using S = Smem<D>;
+  constexpr int kNP = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready, done;
+  __shared__ uint32_t tmem_base;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT;
+  unsigned x = blockIdx.x;  // (sequence, k/v head, query tiles from the last down, heads of the group)
+  const int g = x % G;
+  x /= G;
+  const int qt = tiles - 1 - static_cast<int>(x % tiles);
+  x /= tiles;
+  const int kvh = x % p.Hkv, b = x / p.Hkv;
+  const int len = window::seq_len(p, b), t0 = qt * kT;
+  if (t0 >= len) return;
+  const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kT, len) - 1, p.window, p.n_sink);
+  const int n = kt.count(), qrow = b * p.H + kvh * G + g;
+
+  if (tid == 0) {
+    sm100::mbar_init(&q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&k_full[i], 1), sm100::mbar_init(&k_empty[i], 1);
+      sm100::mbar_init(&v_full[i], 1), sm100::mbar_init(&v_empty[i], 1);
+    }
+    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&s_free, 256);
+    sm100::mbar_init(&dp_ready[0], 1), sm100::mbar_init(&dp_ready[1], 1), sm100::mbar_init(&ds_ready, 256);
+    sm100::mbar_init(&done, 1);
+    sm100::fence_mbar_init();
+  }
+  if (warp == 9) {
+    sm100::tmem_alloc(&tmem_base, 512);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;  // dP: two buffers of 128 columns
+  bool fine = true;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------------------------ loads
+    if (lane == 0) {
+      sm100::prefetch_tmap(&tm_k), sm100::prefetch_tmap(&tm_v);
+      sm100::mbar_arrive_expect_tx(&q_full, 2 * S::kTile);
+      load_tile<kNP>(sm + S::kFixed, &tm_q, &q_full, t0, qrow);
+      load_tile<kNP>(sm + S::kFixed + S::kTile, &tm_do, &q_full, t0, qrow);
+      int it = 0;
+      bool k_sent = false;
+      for (; it < n; ++it) {
+        const int slot = it & 1, round = it >> 1, j0 = kt.walk(it) * kT, row = b * p.Hkv + kvh;
+        k_sent = false;
+        if (round > 0) fine = sm100::mbar_wait_bounded(&k_empty[slot], (round - 1) & 1, kWaitCycles);
+        if (!fine) break;
+        sm100::mbar_arrive_expect_tx(&k_full[slot], S::kTile);
+        load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_k, &k_full[slot], j0, row);
+        k_sent = true;
+        if (round > 0) fine = sm100::mbar_wait_bounded(&v_empty[slot], (round - 1) & 1, kWaitCycles);
+        if (!fine) break;
+        sm100::mbar_arrive_expect_tx(&v_full[slot], S::kTile);
+        load_tile<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, &tm_v, &v_full[slot], j0, row);
+      }
+      if (!fine) {  // nothing of this CTA may be in flight when it ends
+        sm100::mbar_wait_bounded(&q_full, 0, kWaitCycles);
+        for (int back = it > 1 ? it - 1 : 0; back <= it && back < n; ++back) {
+          if (back < it || k_sent) sm100::mbar_wait_bounded(&k_full[back & 1], (back >> 1) & 1, kWaitCycles);
+          if (back < it) sm100::mbar_wait_bounded(&v_full[back & 1], (back >> 1) & 1, kWaitCycles);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------------------------ products
+    const uint32_t q_addr = sm100::smem_u32(sm + S::kFixed), do_addr = q_addr + S::kTile;
+    const uint32_t ring = sm100::smem_u32(sm + S::kRing);
+    // S and dP of tile ``it``; k and v rows behind the end are zeroed (their weights are zero)
+    auto issue = [&](int it) {
+      const int slot = it & 1, inside = len - kt.walk(it) * kT;
+      if (inside < kT) {
+        zero_rows<kNP>(sm + S::kRing + 2 * slot * S::kTile, inside, lane);
+        zero_rows<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, inside, lane);
+      }
+      if (lane == 0) {
+        mma_rows<D>(t_s, q_addr, ring + 2 * slot * S::kTile);
+        sm100::mma_commit(&s_ready);
+        mma_rows<D>(t_dp + 128 * slot, do_addr, ring + (2 * slot + 1) * S::kTile);
+        sm100::mma_commit(&dp_ready[slot]);
+        sm100::mma_commit(&v_empty[slot]);
+      }
+    };
+    fine = warp_wait(&q_full, 0) && warp_wait(&k_full[0], 0) && warp_wait(&v_full[0], 0);
+    if (fine) issue(0);
+    for (int it = 0; it < n && fine; ++it) {
+      const int slot = it & 1, next = (it + 1) & 1, next_round = (it + 1) >> 1;
+      if (it + 1 < n) {
+        fine = warp_wait(&k_full[next], next_round & 1) && warp_wait(&v_full[next], next_round & 1) && warp_wait(&s_free, it & 1);
+        if (!fine) break;
+        sm100::tc_fence_after();
+        issue(it + 1);
+      }
+      fine = warp_wait(&ds_ready, it & 1);
+      if (!fine) break;
+      sm100::tc_fence_after();
+      if (lane == 0) {
+        mma_weights<D>(t_dq, t_dp + 128 * slot, 64, ring + 2 * slot * S::kTile, it > 0);
+        sm100::mma_commit(&k_empty[slot]);
+      }
+    }
+    if (lane == 0) {
+      sm100::mma_commit(&done);
+      if (!fine) sm100::mbar_wait_bounded(&done, 0, kWaitCycles);
+    }
+  } else {
+    // ------------------------------------------------------------------------------------ weights
+    const int half = warp >> 2, t = t0 + (tid & 127);
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const float c = p.scale * kLog2e;
+    const int w_first = t0 + 32 * (warp & 3), w_last = w_first + 31;
+    const float2 r = t < len ? rows[(size_t)qrow * p.L + t] : make_float2(0.f, 0.f);
+    for (int it = 0; it < n; ++it) {
+      const int j0 = kt.walk(it) * kT + 64 * half;
+      fine = warp_wait(&s_ready, it & 1);
+      if (!fine) break;
+      sm100::tc_fence_after();
+      float s[2][32];
+      sm100::tmem_ld32(t_s + lanes + 64 * half, s[0]);
+      sm100::tmem_ld32(t_s + lanes + 64 * half + 32, s[1]);
+      sm100::tmem_wait_ld();
+      sm100::tc_fence_before();
+      sm100::mbar_arrive(&s_free);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[u][e] = exp2_fast(fmaf(s[u][e], c, -r.x));
+      const bool all_seen = j0 + 63 <= w_first && (w_last - j0 < p.window || j0 + 64 <= p.n_sink);
+      if (!all_seen) {
+        const int hi = t - j0, lo = hi - p.window, sinks = p.n_sink - j0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = 32 * u + e;
+            if (col > hi || (col <= lo && col >= sinks)) s[u][e] = 0.f;
+          }
+      }
+      fine = warp_wait(&dp_ready[it & 1], (it >> 1) & 1);
+      if (!fine) break;
+      sm100::tc_fence_after();
+      const uint32_t t_mine = t_dp + 128 * (it & 1) + lanes + 64 * half;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float dp[32], w[16];
+        sm100::tmem_ld32(t_mine + 32 * u, dp);
+        sm100::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = __uint_as_float(pack_bf16(s[u][2 * e] * (dp[2 * e] - r.y), s[u][2 * e + 1] * (dp[2 * e + 1] - r.y)));
+        sm100::tmem_st16(t_mine + 16 * u, w);
+      }
+      sm100::tmem_wait_st();
+      sm100::tc_fence_before();
+      sm100::mbar_arrive(&ds_ready);
+    }
+    if (fine) {
+      fine = warp_wait(&done, 0);
+      sm100::tc_fence_after();
+    }
+    if (fine) {  // each half writes half of the columns
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq) + ((size_t)qrow * p.L + t) * D + half * (D / 2);
+#pragma unroll 1
+      for (int u = 0; u < D / 2; u += 32) {
+        float a[32];
+        sm100::tmem_ld32(t_dq + lanes + half * (D / 2) + u, a);
+        sm100::tmem_wait_ld();
+        if (t < len) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(out + u + 8 * e) = pack8_bf16(a + 8 * e, p.scale);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (!fine) raise_status(p.status, kStatusTimeout);
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) sm100::tmem_dealloc(tmem, 512);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// One or two sink tiles: cut their walk (every later query tile) into parts of a regular tile's walk.
+KeyPass key_pass(int H, int Hkv, int L, int window, int n_sink) {
+  const int tiles = (L + kT - 1) / kT, sinks = n_sink > 0 ? (n_sink < L ? (n_sink - 1) / kT + 1 : tiles) : 0;
+  KeyPass kp{0, 1, nullptr};
+  if (sinks == 0 || sinks > 2 || sinks >= tiles) return kp;
+  const int regular = (window - 1) / kT + 2;  // query tiles that see a tile within the window
+  int parts = (tiles + regular - 1) / regular;
+  const int items = tiles * (H / Hkv);
+  if (parts > 64) parts = 64;
+  if (parts > items / 4) parts = items / 4;  // a part shorter than four tiles is all start-up
+  if (parts < 2) return kp;
+  kp.sinks = sinks, kp.parts = parts;
+  return kp;
+}
+
+struct Layout {
+  size_t rows, dO, part, end;  // byte offsets in the scratch
+};
+Layout layout(int B, int H, int Hkv, int L, int D, int out_dtype, const KeyPass& kp) {
+  Layout l{};
+  const size_t tokens = (size_t)B * H * L;
+  l.rows = 0, l.dO = round256(tokens * sizeof(float2));
+  l.part = l.dO + (out_dtype == kF32 ? round256(tokens * D * 2) : 0);
+  l.end = l.part + (kp.sinks ? round256((size_t)B * Hkv * kp.sinks * kp.parts * 2 * kT * D * sizeof(float)) : 0);
+  return l;
+}
+
+template <int D>
+cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
+  KeyPass kp = key_pass(p.H, p.Hkv, p.L, p.window, p.n_sink);
+  const Layout l = layout(p.B, p.H, p.Hkv, p.L, D, p.out_dtype, kp);
+  char* scratch = static_cast<char*>(p.scratch);
+  float2* rows = reinterpret_cast<float2*>(scratch + l.rows);
+  __nv_bfloat16* dO16 = reinterpret_cast<__nv_bfloat16*>(scratch + l.dO);
+  kp.part = reinterpret_cast<float*>(scratch + l.part);
+  CUtensorMap tq, tk, tv, td;
+  if (!make_bf16_tmap_rows(&tq, p.q, p.B * p.H, p.L, D, kT) || !make_bf16_tmap_rows(&tk, p.k, p.B * p.Hkv, p.L, D, kT) ||
+      !make_bf16_tmap_rows(&tv, p.v, p.B * p.Hkv, p.L, D, kT) ||
+      !make_bf16_tmap_rows(&td, p.out_dtype == kBF16 ? p.dO : dO16, p.B * p.H, p.L, D, kT))
+    return cudaErrorInvalidValue;
+  const size_t tokens = (size_t)p.B * p.H * p.L;
+  window_rows_kernel<D><<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(p, rows, dO16);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int smem = Smem<D>::kTotal + 1024, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
+  e = cudaFuncSetAttribute(window_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(window_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long keys = (long long)bh * (kp.sinks * kp.parts + tiles - kp.sinks);
+  window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, kp);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  window_dq_tc_kernel<D><<<(unsigned)((long long)p.B * p.H * tiles), kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || kp.sinks == 0) return e;
+  const size_t words = (size_t)bh * kp.sinks * 2 * kT * D / 8;
+  window_join_kernel<D><<<(unsigned)((words + 255) / 256), 256, 0, stream>>>(p, kp);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_bwd_tc_scratch_bytes(int B, int H, int Hkv, int L, int d, int out_dtype, int window, int n_sink) {
+  return layout(B, H, Hkv, L, d, out_dtype, key_pass(H, Hkv, L, window < L ? window : L, n_sink < L ? n_sink : L)).end;
+}
+
+cudaError_t launch_window_bwd_tc(int d, const WindowArgs& p, cudaStream_t stream) {
+  return d == 128 ? backward<128>(p, stream) : backward<64>(p, stream);
+}
+
+}  // namespace kdn

@@ -109,7 +109,7 @@ def lib() -> ctypes.CDLL:
     pages = ctypes.POINTER(PagesC)
     L.kdn_window_attn.argtypes = [dims, i, vp, vp, vp, vp, i, i, f, vp, vp, vp, sz, vp]
     L.kdn_window_attn_backward.argtypes = [dims, i, vp, vp, vp, vp, i, i, f] + [vp] * 7 + [sz, vp]
-    L.kdn_window_workspace_bytes.argtypes = [dims, i, i, i]
+    L.kdn_window_workspace_bytes.argtypes = [dims, i, i, i, i]
     L.kdn_pages_reserve.argtypes = [pages, i, vp, vp, i, vp, sz, vp]
     L.kdn_pages_fork.argtypes = [pages, i, vp, vp, vp, vp, sz, vp]
     L.kdn_pages_free.argtypes = [pages, i, vp, vp, sz, vp]
@@ -534,9 +534,9 @@ def _window_args(q, k, v, lens, scale):
     return B, H, Hkv, L, dk, dv, dev, float(dk ** -0.5 if scale is None else scale)
 
 
-def window_workspace_bytes(B, H, Hkv, L, dk, dv, n_sink=0, in_dtype=torch.bfloat16, out_dtype=None, backward=False):
+def window_workspace_bytes(B, H, Hkv, L, dk, dv, window, n_sink=0, in_dtype=torch.bfloat16, out_dtype=None, backward=False):
     d = Dims(B, H, L, dk, dv, 0, _DTYPES[in_dtype], _DTYPES[out_dtype or in_dtype], 0)
-    return int(lib().kdn_window_workspace_bytes(ctypes.byref(d), Hkv, n_sink, int(backward)))
+    return int(lib().kdn_window_workspace_bytes(ctypes.byref(d), Hkv, window, n_sink, int(backward)))
 
 
 def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=None, workspace=None, out_dtype=None,
@@ -558,7 +558,7 @@ def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=No
             o = new(B, H, L, dv, dtype=out_dtype, device=dev)
         if lse is None:
             lse = new(B, H, L, dtype=torch.float32, device=dev)
-        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, n_sink, 0), dev)
+        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, window, n_sink, 0), dev)
     _need(o, "o", (B, H, L, dv), out_dtype, dev)
     _need(lse, "lse", (B, H, L), torch.float32, dev)
     st = lib().kdn_window_attn(ctypes.byref(dims), Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(lens), window, n_sink, scale,
@@ -584,7 +584,7 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
         dq = new(B, H, L, d_k, dtype=q.dtype, device=dev) if dq is None else dq
         dk = new(B, Hkv, L, d_k, dtype=q.dtype, device=dev) if dk is None else dk
         dv = new(B, Hkv, L, d_v, dtype=q.dtype, device=dev) if dv is None else dv
-        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, n_sink, 1), dev)
+        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, window, n_sink, 1), dev)
     _need(dq, "dq", (B, H, L, d_k), q.dtype, dev)
     _need(dk, "dk", (B, Hkv, L, d_k), q.dtype, dev)
     _need(dv, "dv", (B, Hkv, L, d_v), q.dtype, dev)

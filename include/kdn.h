@@ -295,7 +295,7 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
  * enter the second product as bf16; sums, maxima and both products' accumulators are fp32), everything else
- * on the fp32 cores.  workspace: kdn_window_workspace_bytes(dims, kv_heads, n_sink, 0) bytes.  Asynchronous. */
+ * on the fp32 cores.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 0) bytes.  Asynchronous. */
 KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
                            const int* lens, int window, int n_sink, float scale, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);
@@ -307,14 +307,15 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
  * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
  * gradients do not change from run to run.  Rows behind a sequence's last token are left as they were; lse has
- * no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, n_sink, 1) bytes. */
+ * no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
                                     const void* v, const int* lens, int window, int n_sink, float scale,
                                     const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace of kdn_window_attn (backward = 0) or kdn_window_attn_backward (1); 0 for invalid dims. */
-KDN_EXPORT size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int n_sink, int backward);
+KDN_EXPORT size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int window, int n_sink,
+                                             int backward);
 
 /* The books of a paged key-value cache.  Keys and values of all sequences lie in pages of page_size tokens,
  *   k_pages [num_pages, kv_heads, page_size, d_k],  v_pages [num_pages, kv_heads, page_size, d_v]  (16-byte aligned),

@@ -80,9 +80,9 @@ def test_window_attention_refusals(L):
     assert _attn(L, d) == kdn.KDN_ERR_INVALID_ARG and b"q is NULL" in L.kdn_last_error()
     args = [None] * 3 + [None, 4, 0, 1.0] + [None] * 7 + [0, None]
     assert L.kdn_window_attn_backward(ctypes.byref(d), 1, *args) == kdn.KDN_ERR_INVALID_ARG
-    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 3, 0, 1) == 0
-    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 0, 0) >= 256
-    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 0, 1) >= 256 + 4 * 8 * 4
+    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 3, 4, 0, 1) == 0
+    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 4, 0, 0) >= 256
+    assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 4, 0, 1) >= 256 + 4 * 8 * 4
 
 
 def test_paged_cache_refusals(L):

@@ -98,6 +98,16 @@ def test_shared_heads(H, Hkv, dtype):
     _check(*_inputs(2, H, Hkv, 300, 64, 64, dtype, seed=5), 90, 9)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_sink", [1, 128, 200, 300])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (4, 2)])
+def test_sinks_of_a_long_sequence(d, n_sink, H, Hkv):
+    """One or two sink tiles whose walk over the later queries is cut into parts (and three, where it is not), in a
+    batch whose shorter sequences leave some parts empty."""
+    lens = torch.tensor([1700, 1700, 130, 0], dtype=torch.int32, device=DEV)
+    _check(*_inputs(4, H, Hkv, 1700, d, d, torch.bfloat16, seed=16), 60, n_sink, lens)
+
+
 @pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.bfloat16, 64), (torch.bfloat16, 128)])
 @pytest.mark.parametrize("window,n_sink", [(50, 4), (1000, 0), (130, 140)])
 def test_padded_batch_with_nan_behind_the_sequences(dtype, d, window, n_sink):
