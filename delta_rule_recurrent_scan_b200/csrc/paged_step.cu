@@ -9,6 +9,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "sm100.cuh"
 #include "window.cuh"
 
 namespace kdn {
@@ -51,13 +52,13 @@ constexpr int kTok = 32, kThr = 128, kHB = 8;
 
 template <int D>
 __device__ __forceinline__ bool stage_tokens(float* dst, const void* pool, const PagedStepArgs& p, const int* entries, int kvh,
-                                             int j0, int n) {
+                                             int j0, int n, int win) {
   constexpr int Q = D / 4;
   bool bad = false;
   for (int e = threadIdx.x; e < kTok * Q; e += kThr) {
     const int r = e / Q, c = 4 * (e % Q), j = j0 + r;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < n) {
+    if (j < n && window::visible(n - 1, j, win, p.n_sink)) {  // the pages of hidden tokens are not asked for
       const int page = entries[j / p.page_size];
       if (page < 0 || page >= p.num_pages) {
         bad = true;
@@ -103,8 +104,8 @@ __global__ void __launch_bounds__(kThr) paged_step_kernel(PagedStepArgs p) {
   for (int it = it0; it < it1; ++it) {
     const int j0 = kt.walk(it) * kTok;
     __syncthreads();
-    bad |= stage_tokens<DK>(k_s, p.k_pages, p, entries, w.kvh, j0, n);
-    bad |= stage_tokens<DV>(v_s, p.v_pages, p, entries, w.kvh, j0, n);
+    bad |= stage_tokens<DK>(k_s, p.k_pages, p, entries, w.kvh, j0, n, win);
+    bad |= stage_tokens<DV>(v_s, p.v_pages, p, entries, w.kvh, j0, n, win);
     __syncthreads();
     float s[2] = {0.f, 0.f};
 #pragma unroll 8
@@ -181,6 +182,241 @@ __global__ void __launch_bounds__(kThr) paged_step_kernel(PagedStepArgs p) {
   }
 }
 
+// ------------------------------------------------------------------------------------------ bf16, warp matrix products
+// d_k = d_v = 64 or 128.  The step reads every visible key and value once and does two multiply-adds per element and
+// query head, so it is bound by memory; products on whole 128-row tensor-core tiles would be nearly all padding (a k/v
+// head has 1 to 16 query heads), the warp's m16 n8 k16 product fits: rows = query heads, columns = tokens, then columns
+// = d_v.  Each of 4 warps walks units of 16 tokens with a pipeline of its own (cp.async into kStages swizzled stages,
+// no CTA barrier) and its own running maximum, sum and o; the warps are joined through shared memory at the end.
+//
+// The weights enter the second product as bf16 hi + lo (2^-16 of a weight): with up to 8 query heads the 16 rows hold
+// every head twice, rows 0-7 taking hi and rows 8-15 lo, so the pair costs nothing; with 9 to 16 heads two products.
+constexpr int kMT = 16, kMWarps = 4, kStages = 3, kMHB = 16;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes, or zeros where !there.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D>
+struct StepSmem {
+  static constexpr int kTile = kMT * D * 2;            // 16 tokens of k or of v
+  static constexpr int kWarp = kStages * 2 * kTile;
+  static constexpr int kTotal = kMWarps * kWarp;
+  static_assert(kMWarps * kMHB * D * 4 <= kTotal, "the warps' o are joined in the same memory");
+};
+
+template <int D, bool TWICE>
+__global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepArgs p, int shift) {
+  using Sm = StepSmem<D>;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ float m_s[kMWarps][kMHB], l_s[kMWarps][kMHB];
+  constexpr int kChunks = D / 8;                       // 16-byte words of a row
+  constexpr int kRows = 32 / kChunks;                  // rows a warp copies at once
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const Part w = which<kMHB>(p);
+  const int r = p.row ? p.row[w.b] : w.b;
+  int n = 0;
+  const int* entries = nullptr;
+  bool bad = r < 0 || r >= p.rows;
+  if (!bad) {
+    n = static_cast<int>(min((long long)max(p.lens[r], 0), (long long)p.max_pages << shift));
+    entries = p.table + (size_t)r * p.max_pages;
+  }
+  const int win = p.window > 0 ? p.window : INT_MAX;
+  KeyTiles kt{0, 0, 0};
+  if (n > 0) kt = window::key_tiles<kMT>(n - 1, n - 1, win, p.n_sink);
+  const int u0 = (int)((long long)kt.count() * w.split / p.splits) + warp;
+  const int u1 = (int)((long long)kt.count() * (w.split + 1) / p.splits);
+
+  // this lane's rows of the units it copies
+  const int chunk = lane % kChunks, row0 = lane / kChunks;
+  const uint32_t stage0 = static_cast<uint32_t>(__cvta_generic_to_shared(sm)) + warp * Sm::kWarp;
+  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.k_pages);
+  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(p.v_pages);
+  const int mask = p.page_size - 1;
+  const bool one_page = p.page_size >= kMT;            // a unit lies in one page
+  // the page of a unit's first token, looked up a step ahead of its copies
+  auto look = [&](int u) { return u < u1 && one_page ? entries[(kt.walk(u) * kMT) >> shift] : 0; };
+  auto issue = [&](int u, int stage, int entry) {
+    if (u < u1) {
+      const int j0 = kt.walk(u) * kMT;
+      const uint32_t dst = stage0 + stage * 2 * Sm::kTile;
+      const bool full = j0 + kMT <= n && (n - 1 - j0 < win || j0 + kMT <= p.n_sink);
+#pragma unroll
+      for (int i = 0; i < kMT / kRows; ++i) {
+        const int row = row0 + i * kRows, j = j0 + row;
+        bool there = full || (j < n && window::visible(n - 1, j, win, p.n_sink));
+        const int page = one_page ? entry : (there ? entries[j >> shift] : 0);
+        if (there && (page < 0 || page >= p.num_pages)) bad = true, there = false;
+        const size_t at = there ? ((((size_t)page * p.Hkv + w.kvh) << shift) + (j & mask)) * D + 8 * chunk : 0;
+        const uint32_t to = dst + row * (D * 2) + ((chunk ^ (row & 7)) << 4);
+        copy16_or_zero(to, kp + at, there);
+        copy16_or_zero(to + Sm::kTile, vp + at, there);
+      }
+    }
+    async_commit();
+  };
+  int entry = look(u0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    const int next = look(u0 + (i + 1) * kMWarps);
+    issue(u0 + i * kMWarps, i, entry);
+    entry = next;
+  }
+
+  // q as the first product's A operand
+  uint32_t q[D / 16][4];
+  {
+    const uint32_t* qp = reinterpret_cast<const uint32_t*>(p.q) + ((size_t)w.b * p.H + w.h0) * (D / 2);
+    const int ra = g, rb = TWICE ? g : g + 8;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      q[ks][0] = ra < w.nh ? qp[ra * (D / 2) + 8 * ks + t4] : 0u;
+      q[ks][1] = rb < w.nh ? qp[rb * (D / 2) + 8 * ks + t4] : 0u;
+      q[ks][2] = ra < w.nh ? qp[ra * (D / 2) + 8 * ks + t4 + 4] : 0u;
+      q[ks][3] = rb < w.nh ? qp[rb * (D / 2) + 8 * ks + t4 + 4] : 0u;
+    }
+  }
+  const float c2 = p.scale * kLog2e;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g and g + 8 (base 2); l of this lane's tokens
+  float o[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+  int stage = 0;
+  for (int u = u0; u < u1; u += kMWarps) {
+    async_wait<kStages - 2>();
+    __syncwarp();
+    {  // the stage read last is free for all lanes: its copies go out first
+      const int ahead = u + (kStages - 1) * kMWarps;
+      const int next = look(ahead + kMWarps);
+      issue(ahead, stage == 0 ? kStages - 1 : stage - 1, entry);
+      entry = next;
+    }
+    const uint32_t k_at = stage0 + stage * 2 * Sm::kTile, v_at = k_at + Sm::kTile;
+    float s[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      const int row = ((lane >> 4) << 3) + (lane & 7), c = 2 * ks + ((lane >> 3) & 1);
+      uint32_t b[4];
+      ldsm4(b, k_at + row * (D * 2) + ((c ^ (row & 7)) << 4));
+      mma16816(s[0], q[ks], b[0], b[1]);
+      mma16816(s[1], q[ks], b[2], b[3]);
+    }
+    const int j0 = kt.walk(u) * kMT;
+    if (!(j0 + kMT <= n && (n - 1 - j0 < win || j0 + kMT <= p.n_sink))) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + 8 * i + 2 * t4 + (e & 1);
+          if (j >= n || !window::visible(n - 1, j, win, p.n_sink)) s[i][e] = -INFINITY;
+        }
+    }
+    float base[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1])) * c2;
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = fmaxf(top, m[i]);
+      base[i] = top == -INFINITY ? 0.f : top;
+      const float keep = exp2_fast(m[i] - base[i]);
+      if (__any_sync(0xffffffffu, top != m[i])) {
+        l[i] *= keep;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) o[d][2 * i] *= keep, o[d][2 * i + 1] *= keep;
+      }
+      m[i] = top;
+    }
+    uint32_t hi[4], lo[4];  // P as the second product's A operand: (row g, row g + 8) x (tokens 0-7, 8-15)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float a = exp2_fast(fmaf(s[i][2 * h], c2, -base[h])), b = exp2_fast(fmaf(s[i][2 * h + 1], c2, -base[h]));
+        l[h] += a + b;
+        sm100::split2_bf16(a, b, hi[2 * i + h], lo[2 * i + h]);
+      }
+    if constexpr (TWICE) hi[1] = lo[1], hi[3] = lo[3];
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const int row = (((lane >> 3) & 1) << 3) + (lane & 7), c = 2 * d + (lane >> 4);
+      uint32_t b[4];
+      ldsm4_t(b, v_at + row * (D * 2) + ((c ^ (row & 7)) << 4));
+      mma16816(o[2 * d], hi, b[0], b[1]);
+      mma16816(o[2 * d + 1], hi, b[2], b[3]);
+      if constexpr (!TWICE) {
+        mma16816(o[2 * d], lo, b[0], b[1]);
+        mma16816(o[2 * d + 1], lo, b[2], b[3]);
+      }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  bad = __syncthreads_or(bad);  // every warp has read its last stage
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (t4 == 0) m_s[warp][g + 8 * i] = m[i], l_s[warp][g + 8 * i] = bad ? NAN : l[i];
+  }
+  float* o_s = reinterpret_cast<float*>(sm);  // [warp][row][D]
+#pragma unroll
+  for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<float2*>(o_s + ((size_t)warp * kMHB + g + 8 * i) * D + 8 * d + 2 * t4) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+  __syncthreads();
+  for (int e = tid; e < w.nh * D; e += 32 * kMWarps) {
+    const int h = e / D, col = e % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMWarps; ++i) M = fmaxf(M, m_s[i][h]);
+    const float b = M == -INFINITY ? 0.f : M;
+    float sum = 0.f, x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMWarps; ++i) {
+      const float f = exp2_fast(m_s[i][h] - b);
+      float v = o_s[(i * kMHB + h) * D + col];
+      if constexpr (TWICE) v += o_s[(i * kMHB + h + 8) * D + col];
+      sum = fmaf(f, l_s[i][h], sum);
+      x = fmaf(f, v, x);
+    }
+    const size_t head = (size_t)w.b * p.H + w.h0 + h;
+    if (p.splits == 1) {
+      store_elem(p.o, head * D + col, sum == 0.f ? 0.f : x / sum, p.out_dtype);
+      if (col == 0 && p.lse) p.lse[head] = M * kLn2 + logf(sum);
+    } else {
+      const size_t at = part_at(p, w.b, w.h0 + h, w.split);
+      p.part[at * D + col] = x;
+      if (col == 0) part_max(p, D)[at] = M * kLn2, part_sum(p, D)[at] = sum;
+    }
+  }
+}
+
 // Joins a head's parts: one CTA of d_v threads (at least a warp) per head.
 template <int DV>
 __global__ void __launch_bounds__(DV < 32 ? 32 : DV) paged_join_kernel(PagedStepArgs p) {
@@ -213,6 +449,24 @@ cudaError_t step(const PagedStepArgs& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+bool step_mma_supported(int dk, int dv, int in_dtype) { return in_dtype == kBF16 && dk == dv && (dk == 64 || dk == 128); }
+
+template <int D>
+cudaError_t step_mma(const PagedStepArgs& p, cudaStream_t stream) {
+  const int G = p.H / p.Hkv;
+  const long long ctas = (long long)p.n * p.Hkv * ((G + kMHB - 1) / kMHB) * p.splits;
+  int shift = 0;
+  while ((1 << shift) < p.page_size) ++shift;
+  const auto kernel = G <= 8 ? paged_step_mma_kernel<D, true> : paged_step_mma_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, StepSmem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)ctas, 32 * kMWarps, StepSmem<D>::kTotal, stream>>>(p, shift);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  paged_join_kernel<D><<<p.n * p.H, D, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename F>
 cudaError_t for_dim(int d, F f) {
   switch (d) {
@@ -227,13 +481,20 @@ cudaError_t for_dim(int d, F f) {
 }  // namespace
 
 int paged_step_splits(int dk, int dv, int in_dtype, int n, int H, int Hkv, long long most_tokens) {
-  (void)dk, (void)dv, (void)in_dtype;
   const int G = H / Hkv;
-  const long long pairs = (long long)n * Hkv * ((G + kHB - 1) / kHB);
-  const long long tiles = (most_tokens + kTok - 1) / kTok;
-  // enough parts for four CTAs on each of 148 SMs, of at least four tiles each
-  long long s = (4 * 148 + pairs - 1) / pairs;
-  if (s > tiles / 4) s = tiles / 4;
+  long long s;
+  if (step_mma_supported(dk, dv, in_dtype)) {
+    // Two CTAs fit an SM.  With few (sequence, k/v head) pairs one wave of equal parts; with many, several waves, so that
+    // sequences of different lengths even out.  A part has at least 128 tokens, or its start-up outweighs it.
+    const long long pairs = (long long)n * Hkv * ((G + kMHB - 1) / kMHB), slots = 2 * 148;
+    s = 2 * pairs <= slots ? slots / pairs : (6 * slots + pairs - 1) / pairs;
+    if (s > most_tokens / 128) s = most_tokens / 128;
+  } else {
+    // enough parts for four CTAs on each of 148 SMs, of at least four tiles each
+    const long long pairs = (long long)n * Hkv * ((G + kHB - 1) / kHB), tiles = (most_tokens + kTok - 1) / kTok;
+    s = (4 * 148 + pairs - 1) / pairs;
+    if (s > tiles / 4) s = tiles / 4;
+  }
   return s < 1 ? 1 : (int)s;
 }
 
@@ -242,6 +503,7 @@ size_t paged_step_part_floats(int dv, int n, int H, int splits) {
 }
 
 cudaError_t launch_paged_step(int dk, int dv, const PagedStepArgs& p, cudaStream_t stream) {
+  if (step_mma_supported(dk, dv, p.in_dtype)) return dk == 128 ? step_mma<128>(p, stream) : step_mma<64>(p, stream);
   return for_dim(dk, [&](auto k) { return for_dim(dv, [&](auto v) { return step<k(), v()>(p, stream); }); });
 }
 

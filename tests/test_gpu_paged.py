@@ -173,6 +173,20 @@ def test_chosen_rows_and_broken_entries(dtype, d):
     assert torch.equal(o, kdn.paged_attn_step(q[:1], k, v, table[2:3].contiguous(), _i32([304]))[0])
 
 
+@pytest.mark.parametrize("dtype,d", CASES)
+@pytest.mark.parametrize("page", [1, 4, 16])
+def test_broken_entries_of_hidden_tokens_do_not_matter(dtype, d, page):
+    """Entries right before the window's first token and right behind the sinks, inside the same tiles."""
+    k, v, table, ln, g = _cache([300], 1, d, d, page, dtype, seed=8)
+    q = torch.randn(1, 4, d, generator=g, device=DEV).to(dtype)
+    good = kdn.paged_attn_step(q, k, v, table, ln, window=41, n_sink=3)
+    table[0, -(-3 // page):259 // page] = -7
+    o, lse = kdn.paged_attn_step(q, k, v, table, ln, window=41, n_sink=3)
+    assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+    table[0, 259 // page] = -7
+    assert bool(kdn.paged_attn_step(q, k, v, table, ln, window=41, n_sink=3)[0].isnan().all())
+
+
 def test_step_in_a_graph_follows_the_lengths():
     k, v, table, ln, g = _cache([900, 40], 2, 128, 128, 16, torch.bfloat16, seed=7)
     q = torch.randn(2, 8, 128, generator=g, device=DEV).to(torch.bfloat16)
