@@ -131,11 +131,12 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
   KDN_TRY(check_ptr(o, "o", 16, none));
   KDN_TRY(check_ptr(lse, "lse", 4, none));
   KDN_TRY(check_ptr(lens, "lens", 4, true));
-  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 0)));
+  if (workspace != nullptr) KDN_TRY(check_workspace(workspace, workspace_bytes, kStatusBytes));
+  if (none && workspace == nullptr) return ok();
   DeviceGuard guard;
-  KDN_TRY(use_device_of(workspace, guard));
+  KDN_TRY(use_device_of(none ? workspace : o, guard));
   cudaStream_t st = (cudaStream_t)stream;
-  KDN_TRY(clear_status(workspace, st));
+  if (workspace != nullptr) KDN_TRY(clear_status(workspace, st));
   if (none) return ok();
   kdn::WindowArgs a{};
   a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens;
@@ -294,7 +295,7 @@ kdn_status kdn_paged_attn_step(const kdn_pages* pages, int n, const int* rows, i
   KDN_TRY(check_ptr(o, "o", 16, n == 0));
   KDN_TRY(check_ptr(lse, "lse", 4, true));
   const size_t need = kdn_paged_step_workspace_bytes(pages, n, H, kv_heads, dk, dv, in_dtype, window, n_sink);
-  KDN_TRY(check_workspace(workspace, workspace_bytes, need));
+  if (workspace != nullptr || need > kStatusBytes) KDN_TRY(check_workspace(workspace, workspace_bytes, need));
   if (n == 0) return ok();
   DeviceGuard guard;
   KDN_TRY(use_device_of(k_pages, guard));
@@ -306,7 +307,7 @@ kdn_status kdn_paged_attn_step(const kdn_pages* pages, int n, const int* rows, i
   long long most = (long long)pages->max_pages * pages->page_size;
   if (window > 0 && (long long)window + n_sink < most) most = (long long)window + n_sink;
   a.splits = kdn::paged_step_splits(dk, dv, in_dtype, n, H, kv_heads, most);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+  if (a.splits > 1) a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
   return cuda_status(kdn::launch_paged_step(dk, dv, a, (cudaStream_t)stream), "paged decode step launch");
 }
 

@@ -247,20 +247,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::tc_fence_before();
       sm100::mbar_arrive(&p_ready[i]);
     }
+    const size_t at = ((size_t)b * p.H + hq) * p.L + t;
     if (mine && fine) {
       fine = warp_wait(&done, 0);
       sm100::tc_fence_after();
       if (fine) {
         const float inv = 1.f / l;
-        const size_t at = ((size_t)b * p.H + hq) * p.L + t;
         if (t < len) p.lse[at] = (m + log2f(l)) * kLn2;
 #pragma unroll 1
         for (int u = 0; u < D; u += 32) {
           float o[32];
           sm100::tmem_ld32(t_o + u, o);
           sm100::tmem_wait_ld();
-          if (t >= len) continue;
-          if (p.out_dtype == kBF16) {
+          if (t >= len) {
+          } else if (p.out_dtype == kBF16) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) dst[e] = pack8_bf16(o + 8 * e, inv);
@@ -270,9 +270,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int e = 0; e < 8; ++e)
               dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
           }
+          __syncwarp();
         }
       }
     }
+    if (mine && !fine && t < len) p.lse[at] = NAN;
   }
   if (!fine) raise_status(p.status, kStatusTimeout);
   sm100::tc_fence_before();

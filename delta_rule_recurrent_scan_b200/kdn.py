@@ -139,6 +139,9 @@ def _ptr(t):
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype=None, device=None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.shape == shape and (dtype is None or t.dtype == dtype) and \
+            (device is None or t.device == device) and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -498,16 +501,24 @@ def selftest_wait_timeout(workspace: torch.Tensor | None, wait_cycles: int = 100
 
 # ---------------------------------------------------------------------------------- windowed attention
 
+_SAME = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocations of a call belong to the stream it runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _SAME if stream is None else torch.cuda.stream(stream)
 
 
 def _stream_of(stream, dev):
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(workspace, need, dev):
@@ -558,11 +569,13 @@ def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=No
             o = new(B, H, L, dv, dtype=out_dtype, device=dev)
         if lse is None:
             lse = new(B, H, L, dtype=torch.float32, device=dev)
-        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, window, n_sink, 0), dev)
+    if workspace is not None:
+        _scratch(workspace, 256, dev)
     _need(o, "o", (B, H, L, dv), out_dtype, dev)
     _need(lse, "lse", (B, H, L), torch.float32, dev)
-    st = lib().kdn_window_attn(ctypes.byref(dims), Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(lens), window, n_sink, scale,
-                               _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _stream_of(stream, dev))
+    st = lib().kdn_window_attn(ctypes.byref(dims), Hkv, _at(q), _at(k), _at(v), _at(lens), window, n_sink, scale,
+                               _at(o), _at(lse), _at(workspace), 0 if workspace is None else workspace.numel(),
+                               _stream_of(stream, dev))
     _check(st, "kdn_window_attn")
     return o, lse
 
@@ -588,9 +601,9 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
     _need(dq, "dq", (B, H, L, d_k), q.dtype, dev)
     _need(dk, "dk", (B, Hkv, L, d_k), q.dtype, dev)
     _need(dv, "dv", (B, Hkv, L, d_v), q.dtype, dev)
-    st = lib().kdn_window_attn_backward(ctypes.byref(dims), Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(lens), window, n_sink,
-                                        scale, _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv),
-                                        _ptr(workspace), workspace.numel(), _stream_of(stream, dev))
+    st = lib().kdn_window_attn_backward(ctypes.byref(dims), Hkv, _at(q), _at(k), _at(v), _at(lens), window, n_sink,
+                                        scale, _at(o), _at(lse), _at(dO), _at(dq), _at(dk), _at(dv),
+                                        _at(workspace), workspace.numel(), _stream_of(stream, dev))
     _check(st, "kdn_window_attn_backward")
     return {"dq": dq, "dk": dk, "dv": dv}
 
@@ -649,8 +662,8 @@ def pages_reserve(pages, rows, counts, stream=None):
     each = isinstance(counts, torch.Tensor)
     if each:
         _need(counts, "counts", rows.shape, torch.int32, dev)
-    st = lib().kdn_pages_reserve(ctypes.byref(c), rows.numel(), _ptr(rows), _ptr(counts) if each else None,
-                                 0 if each else counts, _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    st = lib().kdn_pages_reserve(ctypes.byref(c), rows.numel(), _at(rows), _at(counts) if each else None,
+                                 0 if each else counts, _at(ws), ws.numel(), _stream_of(stream, dev))
     _check(st, "kdn_pages_reserve")
 
 
@@ -664,7 +677,7 @@ def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
         if moves is None:
             moves = torch.empty(src_rows.numel(), 2, dtype=torch.int32, device=dev)
     _need(moves, "moves", (src_rows.numel(), 2), torch.int32, dev)
-    st = lib().kdn_pages_fork(ctypes.byref(c), src_rows.numel(), _ptr(src_rows), _ptr(dst_rows), _ptr(moves), _ptr(ws),
+    st = lib().kdn_pages_fork(ctypes.byref(c), src_rows.numel(), _at(src_rows), _at(dst_rows), _at(moves), _at(ws),
                               ws.numel(), _stream_of(stream, dev))
     _check(st, "kdn_pages_fork")
     return moves
@@ -674,7 +687,7 @@ def pages_free(pages, rows, stream=None):
     """Empties the listed rows; pages that no row names any more are free."""
     c, dev, ws = _books(pages, stream)
     _list(rows, "rows", dev)
-    st = lib().kdn_pages_free(ctypes.byref(c), rows.numel(), _ptr(rows), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    st = lib().kdn_pages_free(ctypes.byref(c), rows.numel(), _at(rows), _at(ws), ws.numel(), _stream_of(stream, dev))
     _check(st, "kdn_pages_free")
 
 
@@ -686,7 +699,7 @@ def pages_compact(pages, moves=None, stream=None):
         if moves is None:
             moves = torch.empty(c.num_pages // 2, 2, dtype=torch.int32, device=dev)
     _need(moves, "moves", (c.num_pages // 2, 2), torch.int32, dev)
-    st = lib().kdn_pages_compact(ctypes.byref(c), _ptr(moves), _ptr(ws), ws.numel(), _stream_of(stream, dev))
+    st = lib().kdn_pages_compact(ctypes.byref(c), _at(moves), _at(ws), ws.numel(), _stream_of(stream, dev))
     _check(st, "kdn_pages_compact")
     return moves
 
@@ -708,8 +721,8 @@ def pages_copy(moves, k_pages, v_pages, stream=None):
     num, Hkv, page, dk, dv = _pool(k_pages, v_pages)
     dev = k_pages.device
     _need(moves, "moves", (moves.shape[0], 2), torch.int32, dev)
-    st = lib().kdn_pages_copy(moves.shape[0], _ptr(moves), num, page, Hkv, dk, dv, _DTYPES[k_pages.dtype], _ptr(k_pages),
-                              _ptr(v_pages), _stream_of(stream, dev))
+    st = lib().kdn_pages_copy(moves.shape[0], _at(moves), num, page, Hkv, dk, dv, _DTYPES[k_pages.dtype], _at(k_pages),
+                              _at(v_pages), _stream_of(stream, dev))
     _check(st, "kdn_pages_copy")
 
 
@@ -730,8 +743,8 @@ def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream
     _need(v_new, "v_new", (n, Hkv, T, dv), k_pages.dtype, dev)
     if counts is not None:
         _need(counts, "counts", (n,), torch.int32, dev)
-    st = lib().kdn_pages_write(ctypes.byref(c), n, _ptr(rows), _ptr(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype],
-                               _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _stream_of(stream, dev))
+    st = lib().kdn_pages_write(ctypes.byref(c), n, _at(rows), _at(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype],
+                               _at(k_new), _at(v_new), _at(k_pages), _at(v_pages), _stream_of(stream, dev))
     _check(st, "kdn_pages_write")
 
 
@@ -763,12 +776,13 @@ def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sin
         if lse is None:
             lse = torch.empty(n, H, dtype=torch.float32, device=dev)
         need = lib().kdn_paged_step_workspace_bytes(ctypes.byref(c), n, H, Hkv, dk, dv, _DTYPES[q.dtype], window, n_sink)
-        workspace = _scratch(workspace, need, dev)
+        if workspace is not None or need > 256:
+            workspace = _scratch(workspace, need, dev)
     _need(o, "o", (n, H, dv), out_dtype, dev)
     _need(lse, "lse", (n, H), torch.float32, dev)
     scale = float(dk ** -0.5 if scale is None else scale)
-    st = lib().kdn_paged_attn_step(ctypes.byref(c), n, _ptr(rows), H, Hkv, dk, dv, _DTYPES[q.dtype], _DTYPES[out_dtype],
-                                   _ptr(q), _ptr(k_pages), _ptr(v_pages), window, n_sink, scale, _ptr(o), _ptr(lse),
-                                   _ptr(workspace), workspace.numel(), _stream_of(stream, dev))
+    st = lib().kdn_paged_attn_step(ctypes.byref(c), n, _at(rows), H, Hkv, dk, dv, _DTYPES[q.dtype], _DTYPES[out_dtype],
+                                   _at(q), _at(k_pages), _at(v_pages), window, n_sink, scale, _at(o), _at(lse),
+                                   _at(workspace), 0 if workspace is None else workspace.numel(), _stream_of(stream, dev))
     _check(st, "kdn_paged_attn_step")
     return o, lse

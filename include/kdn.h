@@ -295,7 +295,8 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
  * enter the second product as bf16; sums, maxima and both products' accumulators are fp32), everything else
- * on the fp32 cores.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 0) bytes.  Asynchronous. */
+ * on the fp32 cores.  workspace: 256 bytes for the status word, or NULL: none is kept (a bounded wait that gives
+ * up also leaves NaN in its rows of lse).  Asynchronous. */
 KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
                            const int* lens, int window, int n_sink, float scale, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);
@@ -380,7 +381,7 @@ KDN_EXPORT kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* 
  * NaN.  Long caches are split over the GPU's SMs and the parts joined in a fixed order.  H / kv_heads query heads
  * share a k/v head and read it once.  bf16 pages with d_k = d_v in {64, 128} run on the tensor cores with the
  * softmax weights as bf16 hi + lo pairs.  workspace: kdn_paged_step_workspace_bytes(...) bytes (only scratch: the
- * call has no device status). */
+ * call has no device status), or NULL where that is 256. */
 KDN_EXPORT kdn_status kdn_paged_attn_step(const kdn_pages* pages, int n, const int* rows, int H, int kv_heads, int dk,
                                int dv, kdn_dtype in_dtype, kdn_dtype out_dtype, const void* q, const void* k_pages,
                                const void* v_pages, int window, int n_sink, float scale, void* o, float* lse,
