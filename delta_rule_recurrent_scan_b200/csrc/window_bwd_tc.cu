@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::mbar_init(&q_full[i], 33), sm100::mbar_init(&q_empty[i], 1);  // the copy and 32 lanes' row scalars
       sm100::mbar_init(&do_full[i], 1), sm100::mbar_init(&do_empty[i], 1);
     }
-    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&p_ready, 256);
-    sm100::mbar_init(&dp_ready, 1), sm100::mbar_init(&ds_ready, 256);
+    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&p_ready, 8);
+    sm100::mbar_init(&dp_ready, 1), sm100::mbar_init(&ds_ready, 8);
     sm100::mbar_init(&done, 1);
     sm100::fence_mbar_init();
   }
@@ -189,11 +189,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto end_of = [&](int it) { return len - (lo + (first + it) % per) * kT; };  // rows of this tile inside the sequence
     auto issue_s = [&](int it) {
       if (end_of(it) < kT) zero_rows<kNP>(sm + S::kRing + 2 * (it & 1) * S::kTile, end_of(it), lane);
-      if (lane == 0) mma_rows<D>(t_s, k_addr, q_of(it)), sm100::mma_commit(&s_ready);
+      if (lane == 0) mma_rows<D>(t_s, rows_desc(k_addr), rows_desc(q_of(it))), sm100::mma_commit(&s_ready);
     };
     auto issue_dp = [&](int it) {
       if (end_of(it) < kT) zero_rows<kNP>(sm + S::kRing + (2 * (it & 1) + 1) * S::kTile, end_of(it), lane);
-      if (lane == 0) mma_rows<D>(t_dp, v_addr, do_of(it)), sm100::mma_commit(&dp_ready);
+      if (lane == 0) mma_rows<D>(t_dp, rows_desc(v_addr), rows_desc(do_of(it))), sm100::mma_commit(&dp_ready);
     };
     if (n > 0) {
       fine = warp_wait(&kv_full, 0) && warp_wait(&q_full[0], 0) && warp_wait(&do_full[0], 0);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!fine) break;
       sm100::tc_fence_after();
       if (lane == 0) {
-        mma_weights<D>(t_dv, t_s, 64, do_of(it), it > 0);
+        mma_weights<D>(t_dv, t_s, 64, cols_desc(do_of(it)), it > 0);
         sm100::mma_commit(&do_empty[slot]);
       }
       if (it + 1 < n) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!fine) break;
       sm100::tc_fence_after();
       if (lane == 0) {
-        mma_weights<D>(t_dk, t_dp, 64, q_of(it), it > 0);
+        mma_weights<D>(t_dk, t_dp, 64, cols_desc(q_of(it)), it > 0);
         sm100::mma_commit(&q_empty[slot]);
       }
       if (it + 1 < n) {
@@ -257,14 +257,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           s[u][e + 1] = exp2_fast(fmaf(s[u][e + 1], c, -r.z));
         }
       if (!all_seen) {  // query t sees key j: t >= j and (t < j + window or a sink)
-        const int near = j - t0, far = near + p.window;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {  // 32 queries: all of them see the warp's keys, or some do
+          const int q0 = t0 + 32 * u;
+          if (q0 >= j_last && (q0 + 31 - j_first < p.window || j_last < p.n_sink)) continue;
+          const int near = j - q0, far = near + p.window;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = 32 * u + e;
-            if (col < near || (col >= far && !sink)) s[u][e] = 0.f;
-          }
+          for (int e = 0; e < 32; ++e)
+            if (e < near || (e >= far && !sink)) s[u][e] = 0.f;
+        }
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       sm100::tmem_wait_st();
       sm100::tc_fence_before();
-      sm100::mbar_arrive(&p_ready);
+      warp_arrive(&p_ready);
       fine = warp_wait(&dp_ready, it & 1);
       if (!fine) break;
       sm100::tc_fence_after();
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       sm100::tmem_wait_st();
       sm100::tc_fence_before();
-      sm100::mbar_arrive(&ds_ready);
+      warp_arrive(&ds_ready);
     }
     if (fine) {
       fine = warp_wait(&done, 0);
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float f = half == 0 ? 1.f : p.scale;
       const size_t at = ((size_t)(b * p.Hkv + kvh) * p.L + j) * D;
       float* cut_out = kp.part + ((((size_t)(b * p.Hkv + kvh) * kp.sinks + tile) * kp.parts + part) * 2 + half) * kT * D + key * D;
+      const bool wide = is_wide(half == 0 ? p.dv : p.dk);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half == 0 ? p.dv : p.dk) + at;
 #pragma unroll 1
       for (int u = 0; u < D; u += 32) {
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             *reinterpret_cast<float4*>(cut_out + u + 4 * e) = make_float4(a[4 * e] * f, a[4 * e + 1] * f, a[4 * e + 2] * f, a[4 * e + 3] * f);
         } else if (j < len) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(out + u + 8 * e) = pack8_bf16(a + 8 * e, f);
+          for (int e = 0; e < 32; e += 16) store32(out + u + e, pack8_bf16(a + e, f), pack8_bf16(a + e + 8, f), wide);
         }
         __syncwarp();
       }
@@ -386,8 +388,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::mbar_init(&k_full[i], 1), sm100::mbar_init(&k_empty[i], 1);
       sm100::mbar_init(&v_full[i], 1), sm100::mbar_init(&v_empty[i], 1);
     }
-    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&s_free, 256);
-    sm100::mbar_init(&dp_ready[0], 1), sm100::mbar_init(&dp_ready[1], 1), sm100::mbar_init(&ds_ready, 256);
+    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&s_free, 8);
+    sm100::mbar_init(&dp_ready[0], 1), sm100::mbar_init(&dp_ready[1], 1), sm100::mbar_init(&ds_ready, 8);
     sm100::mbar_init(&done, 1);
     sm100::fence_mbar_init();
   }
@@ -444,9 +446,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         zero_rows<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, inside, lane);
       }
       if (lane == 0) {
-        mma_rows<D>(t_s, q_addr, ring + 2 * slot * S::kTile);
+        mma_rows<D>(t_s, rows_desc(q_addr), rows_desc(ring + 2 * slot * S::kTile));
         sm100::mma_commit(&s_ready);
-        mma_rows<D>(t_dp + 128 * slot, do_addr, ring + (2 * slot + 1) * S::kTile);
+        mma_rows<D>(t_dp + 128 * slot, rows_desc(do_addr), rows_desc(ring + (2 * slot + 1) * S::kTile));
         sm100::mma_commit(&dp_ready[slot]);
         sm100::mma_commit(&v_empty[slot]);
       }
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!fine) break;
       sm100::tc_fence_after();
       if (lane == 0) {
-        mma_weights<D>(t_dq, t_dp + 128 * slot, 64, ring + 2 * slot * S::kTile, it > 0);
+        mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring + 2 * slot * S::kTile), it > 0);
         sm100::mma_commit(&k_empty[slot]);
       }
     }
@@ -490,21 +492,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::tmem_ld32(t_s + lanes + 64 * half + 32, s[1]);
       sm100::tmem_wait_ld();
       sm100::tc_fence_before();
-      sm100::mbar_arrive(&s_free);
+      warp_arrive(&s_free);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 32; ++e) s[u][e] = exp2_fast(fmaf(s[u][e], c, -r.x));
       const bool all_seen = j0 + 63 <= w_first && (w_last - j0 < p.window || j0 + 64 <= p.n_sink);
       if (!all_seen) {
-        const int hi = t - j0, lo = hi - p.window, sinks = p.n_sink - j0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {  // 32 keys: all of the warp's rows see them, or some do
+          const int k0 = j0 + 32 * u;
+          if (k0 + 31 <= w_first && (w_last - k0 < p.window || k0 + 32 <= p.n_sink)) continue;
+          const int hi = t - k0, lo = hi - p.window, sinks = p.n_sink - k0;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = 32 * u + e;
-            if (col > hi || (col <= lo && col >= sinks)) s[u][e] = 0.f;
-          }
+          for (int e = 0; e < 32; ++e)
+            if (e > hi || (e <= lo && e >= sinks)) s[u][e] = 0.f;
+        }
       }
       fine = warp_wait(&dp_ready[it & 1], (it >> 1) & 1);
       if (!fine) break;
@@ -522,13 +525,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       sm100::tmem_wait_st();
       sm100::tc_fence_before();
-      sm100::mbar_arrive(&ds_ready);
+      warp_arrive(&ds_ready);
     }
     if (fine) {
       fine = warp_wait(&done, 0);
       sm100::tc_fence_after();
     }
     if (fine) {  // each half writes half of the columns
+      const bool wide = is_wide(p.dq);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq) + ((size_t)qrow * p.L + t) * D + half * (D / 2);
 #pragma unroll 1
       for (int u = 0; u < D / 2; u += 32) {
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sm100::tmem_wait_ld();
         if (t < len) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(out + u + 8 * e) = pack8_bf16(a + 8 * e, p.scale);
+          for (int e = 0; e < 32; e += 16) store32(out + u + e, pack8_bf16(a + e, p.scale), pack8_bf16(a + e + 8, p.scale), wide);
         }
         __syncwarp();
       }

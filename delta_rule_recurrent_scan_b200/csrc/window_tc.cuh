@@ -35,6 +35,54 @@ __device__ __forceinline__ uint4 pack8_bf16(const float* x, float f) {
                     pack_bf16(x[6] * f, x[7] * f));
 }
 
+// One arrival for a warp, after all its lanes' work (32 single arrivals on one word take turns).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
+}
+
+// 32 bytes to global memory: whole sectors where the array is 32-byte aligned (``wide``; the interface asks for 16).
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = a, static_cast<uint4*>(p)[1] = b;
+  }
+}
+__device__ __forceinline__ bool is_wide(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Division by a number known at launch: q = floor(x / d) for x < 2^31 (multiply by ceil(2^(32 + s) / d), s = ceil(log2 d)).
+struct Divisor {
+  unsigned d, mul, shift;
+  __device__ __forceinline__ unsigned div(unsigned x, unsigned& rest) const {
+    const unsigned q = (__umulhi(x, mul) + x) >> shift;
+    rest = x - q * d;
+    return q;
+  }
+};
+inline Divisor make_divisor(unsigned d) {
+  Divisor v{d, 0, 0};
+  while ((1ull << v.shift) < d) ++v.shift;
+  v.mul = static_cast<unsigned>((((1ull << v.shift) - d) << 32) / d + 1);
+  return v;
+}
+
 // A warp's wait: true when every lane saw the phase complete.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, sm100::mbar_wait_bounded(bar, parity, kWaitCycles));
@@ -60,26 +108,30 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
   for (int pn = 0; pn < NP; ++pn) sm100::tma_load_3d(dst + pn * kPanel, tm, bar, 64 * pn, t0, row);
 }
 
-// D[tmem] (+)= A B^T over D coordinates: A and B tiles of 128 rows in shared memory, both K-major.
+// Descriptors of a tile of 128 rows: as a K-major operand (rows = M or N), and as the MN-major operand of a product over
+// its rows.  A byte offset inside the tile is added to the address field (in 16-byte units), which it cannot overflow.
+__device__ __forceinline__ uint64_t rows_desc(uint32_t tile) { return sm100::smem_desc(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t cols_desc(uint32_t tile) { return sm100::smem_desc(tile, kPanel, 1024); }
+
+// D[tmem] = A B^T over D coordinates: A and B tiles of 128 rows in shared memory (rows_desc).
 template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b) {
   constexpr uint32_t id = sm100::idesc_bf16(128, kT, false, false);
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
-    const uint32_t off = (ks / 4) * kPanel + (ks % 4) * 32;
-    sm100::mma_bf16(d_tmem, sm100::smem_desc(a + off, 16, 1024), sm100::smem_desc(b + off, 16, 1024), id, ks > 0);
+    const uint64_t off = ((ks / 4) * kPanel + (ks % 4) * 32) >> 4;
+    sm100::mma_bf16(d_tmem, a + off, b + off, id, ks > 0);
   }
 }
 
 // D[tmem] (+)= W B: W 128 x 128 bf16 weights in TMEM (pair columns: the first 64 weights at w, the others at w + second),
-// B a tile of 128 rows of D in shared memory.
+// B a tile of 128 rows of D in shared memory (cols_desc).
 template <int D>
-__device__ __forceinline__ void mma_weights(uint32_t d_tmem, uint32_t w, uint32_t second, uint32_t b, bool accumulate) {
+__device__ __forceinline__ void mma_weights(uint32_t d_tmem, uint32_t w, uint32_t second, uint64_t b, bool accumulate) {
   constexpr uint32_t id = sm100::idesc_bf16(128, D, false, true);
 #pragma unroll
   for (int ks = 0; ks < kT / 16; ++ks)
-    sm100::mma_bf16_ts(d_tmem, w + 8 * (ks & 3) + (ks >= 4 ? second : 0u), sm100::smem_desc(b + ks * 2048, kPanel, 1024), id,
-                       accumulate || ks > 0);
+    sm100::mma_bf16_ts(d_tmem, w + 8 * (ks & 3) + (ks >= 4 ? second : 0u), b + (ks * 2048 >> 4), id, accumulate || ks > 0);
 }
 
 }  // namespace window

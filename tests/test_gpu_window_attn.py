@@ -108,6 +108,14 @@ def test_sinks_of_a_long_sequence(d, n_sink, H, Hkv):
     _check(*_inputs(4, H, Hkv, 1700, d, d, torch.bfloat16, seed=16), 60, n_sink, lens)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv", [(5, 12, 4), (7, 7, 7)])
+def test_more_work_than_multiprocessors(d, B, H, Hkv):
+    """Every CTA takes several works in turn, of sequences of all lengths."""
+    lens = torch.tensor([900, 0, 513, 1, 256, 899, 128][:B], dtype=torch.int32, device=DEV)
+    _check(*_inputs(B, H, Hkv, 900, d, d, torch.bfloat16, seed=17), 200, 20, lens)
+
+
 @pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.bfloat16, 64), (torch.bfloat16, 128)])
 @pytest.mark.parametrize("window,n_sink", [(50, 4), (1000, 0), (130, 140)])
 def test_padded_batch_with_nan_behind_the_sequences(dtype, d, window, n_sink):
@@ -195,6 +203,27 @@ def test_empty_sequence_batch_of_none(dtype):
     o, lse = kdn.window_attn(q, k, v, 4)
     g = kdn.window_attn_backward(q, k, v, o, lse, dO, 4)
     assert o.numel() == lse.numel() == g["dq"].numel() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_arrays_on_16_byte_boundaries(d, dtype):
+    """The interface asks for 16-byte alignment, no more: every array here starts 16 bytes behind a larger boundary."""
+    def moved(x):
+        y = torch.empty(x.numel() + 64, dtype=x.dtype, device=DEV)[16 // x.element_size():][:x.numel()].view(x.shape)
+        y.copy_(x)
+        assert y.data_ptr() % 32 == 16
+        return y
+
+    q, k, v, dO = _inputs(1, 2, 1, 200, d, d, dtype, seed=18)
+    o, lse = kdn.window_attn(q, k, v, 70, n_sink=2)
+    g = kdn.window_attn_backward(q, k, v, o, lse, dO, 70, n_sink=2)
+    q, k, v, dO = map(moved, (q, k, v, dO))
+    o1, lse1 = kdn.window_attn(q, k, v, 70, n_sink=2, o=moved(torch.zeros_like(o)))
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)
+    given = {"dq": moved(torch.zeros_like(q)), "dk": moved(torch.zeros_like(k)), "dv": moved(torch.zeros_like(v))}
+    kdn.window_attn_backward(q, k, v, moved(o), lse1, dO, 70, n_sink=2, **given)
+    assert all(torch.equal(given[x], g[x]) for x in g)
 
 
 def test_own_stream_and_captured_graph():
