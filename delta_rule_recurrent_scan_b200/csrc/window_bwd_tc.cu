@@ -36,40 +36,47 @@ struct Smem {
 };
 
 // ------------------------------------------------------------------------------------------ per-query scalars
-// rows[token] = (lse log2(e), delta), and dO as bf16 where it came as fp32.  One warp per token.
+// rows[token] = (-lse log2(e), -delta), and dO as bf16 where it came as fp32.  D / 8 lanes per token.
 template <int D>
 __global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* rows, __nv_bfloat16* dO16) {
-  const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing of this call has raised it yet
-  if (row >= (size_t)p.B * p.H * p.L) return;
-  const int b = static_cast<int>(row / ((size_t)p.H * p.L)), t = static_cast<int>(row % p.L);
-  if (t >= window::seq_len(p, b)) return;
+  constexpr int kLanes = D / 8;
+  const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x, row = e / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  if (e == 0) *p.status = 0;  // nothing of this call has raised it yet
+  bool live = row < (size_t)p.B * p.H * p.L;
+  if (live && p.lens != nullptr) {
+    const size_t head = row / p.L;
+    live = static_cast<int>(row - head * p.L) < window::seq_len(p, static_cast<int>(head / p.H));
+  }
   float x = 0.f;
-  constexpr int E = D / 32;  // 2 or 4 elements per lane
-  float o[E], g[E];
-  const size_t at = row * D + E * lane;
-  if (p.out_dtype == kBF16) {
+  if (live) {
+    float o[8], g[8];
+    const size_t at = row * D + 8 * lane;
+    if (p.out_dtype == kBF16) {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.o) + at);
+      const uint4 c = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO) + at);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const uint32_t a = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.o) + at + e);
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.dO) + at + e);
-      o[e] = __uint_as_float(a << 16), o[e + 1] = __uint_as_float(a & 0xffff0000u);
-      g[e] = __uint_as_float(c << 16), g[e + 1] = __uint_as_float(c & 0xffff0000u);
-    }
-  } else {
+      for (int i = 0; i < 4; ++i) {
+        o[2 * i] = __uint_as_float(aw[i] << 16), o[2 * i + 1] = __uint_as_float(aw[i] & 0xffff0000u);
+        g[2 * i] = __uint_as_float(cw[i] << 16), g[2 * i + 1] = __uint_as_float(cw[i] & 0xffff0000u);
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 a = *reinterpret_cast<const float2*>(static_cast<const float*>(p.o) + at + e);
-      const float2 c = *reinterpret_cast<const float2*>(static_cast<const float*>(p.dO) + at + e);
-      o[e] = a.x, o[e + 1] = a.y, g[e] = c.x, g[e + 1] = c.y;
-      *reinterpret_cast<uint32_t*>(dO16 + at + e) = pack_bf16(c.x, c.y);  // an operand of two bf16 products
+      for (int i = 0; i < 8; i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.o) + at + i);
+        const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.dO) + at + i);
+        o[i] = a.x, o[i + 1] = a.y, o[i + 2] = a.z, o[i + 3] = a.w;
+        g[i] = c.x, g[i + 1] = c.y, g[i + 2] = c.z, g[i + 3] = c.w;
+      }
+      *reinterpret_cast<uint4*>(dO16 + at) = pack8_bf16(g, 1.f);  // an operand of two bf16 products
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x = fmaf(o[i], g[i], x);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) x = fmaf(o[e], g[e], x);
-  x = warp_sum(x);
-  if (lane == 0) rows[row] = make_float2(p.lse[row] * kLog2e, x);
+  for (int i = kLanes / 2; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+  if (live && lane == 0) rows[row] = make_float2(-p.lse[row] * kLog2e, -x);
 }
 
 // ------------------------------------------------------------------------------------------ dk, dv
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kNP = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(16) float2 rows_s[2][kT];
+  __shared__ __align__(16) float rows_s[2][2][kT];  // -lse log2(e), -delta
   __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], s_ready, p_ready, dp_ready, ds_ready, done;
   __shared__ uint32_t tmem_base;
 
@@ -159,11 +166,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_q, &q_full[slot], t0, row);
       }
       q_sent = true;
-      // the rows' scalars; behind the end lse = inf makes every weight zero
+      // the rows' scalars; behind the end -lse = -inf makes every weight zero
 #pragma unroll
       for (int u = 0; u < kT / 32; ++u) {
         const int r = lane + 32 * u;
-        rows_s[slot][r] = t0 + r < len ? rows[(size_t)row * p.L + t0 + r] : make_float2(INFINITY, 0.f);
+        const float2 v = t0 + r < len ? rows[(size_t)row * p.L + t0 + r] : make_float2(-INFINITY, 0.f);
+        rows_s[slot][0][r] = v.x, rows_s[slot][1][r] = v.y;
       }
       sm100::mbar_arrive(&q_full[slot]);
       if (round > 0) fine = warp_wait(&do_empty[slot], (round - 1) & 1);
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------------------------------ weights
     const int half = warp >> 2, key = tid & 127, j = j0 + key;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const float c = p.scale * kLog2e;
+    const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
     const int j_first = j0 + 32 * (warp & 3), j_last = j_first + 31;
     const bool sink = j < p.n_sink;
     for (int it = 0; it < n; ++it) {
@@ -246,15 +254,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::tmem_ld32(t_s + lanes + 64 * half, s[0]);
       sm100::tmem_ld32(t_s + lanes + 64 * half + 32, s[1]);
       sm100::tmem_wait_ld();
-      const float4* rs = reinterpret_cast<const float4*>(&rows_s[it & 1][64 * half]);  // two queries a word
+      const float4* ls = reinterpret_cast<const float4*>(&rows_s[it & 1][0][64 * half]);  // four queries a word
+      const float4* ds = reinterpret_cast<const float4*>(&rows_s[it & 1][1][64 * half]);
       const bool all_seen = t0 >= j_last && (t0 + 63 - j_first < p.window || j_last < p.n_sink);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float4 r = rs[16 * u + e / 2];
-          s[u][e] = exp2_fast(fmaf(s[u][e], c, -r.x));
-          s[u][e + 1] = exp2_fast(fmaf(s[u][e + 1], c, -r.z));
+        for (int e = 0; e < 32; e += 4) {
+          const float4 r = ls[8 * u + e / 4];
+          const float2 x = fma2(make_float2(s[u][e], s[u][e + 1]), c2, make_float2(r.x, r.y));
+          const float2 y = fma2(make_float2(s[u][e + 2], s[u][e + 3]), c2, make_float2(r.z, r.w));
+          s[u][e] = exp2_fast(x.x), s[u][e + 1] = exp2_fast(x.y), s[u][e + 2] = exp2_fast(y.x), s[u][e + 3] = exp2_fast(y.y);
         }
       if (!all_seen) {  // query t sees key j: t >= j and (t < j + window or a sink)
 #pragma unroll
@@ -286,9 +296,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sm100::tmem_ld32(t_dp + lanes + 64 * half + 32 * u, dp);
         sm100::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 r = rs[16 * u + e];
-          w[e] = __uint_as_float(pack_bf16(s[u][2 * e] * (dp[2 * e] - r.y), s[u][2 * e + 1] * (dp[2 * e + 1] - r.w)));
+        for (int e = 0; e < 32; e += 4) {
+          const float4 r = ds[8 * u + e / 4];
+          const float2 x = mul2(make_float2(s[u][e], s[u][e + 1]), add2(make_float2(dp[e], dp[e + 1]), make_float2(r.x, r.y)));
+          const float2 y = mul2(make_float2(s[u][e + 2], s[u][e + 3]), add2(make_float2(dp[e + 2], dp[e + 3]), make_float2(r.z, r.w)));
+          w[e / 2] = __uint_as_float(pack_bf16(x.x, x.y)), w[e / 2 + 1] = __uint_as_float(pack_bf16(y.x, y.y));
         }
         sm100::tmem_st16(t_dp + lanes + 64 * half + 16 * u, w);
       }
@@ -357,40 +369,56 @@ __global__ void __launch_bounds__(256) window_join_kernel(WindowArgs p, KeyPass 
 }
 
 // ------------------------------------------------------------------------------------------ dq
+// One CTA per SM takes work after work (a query tile of a head), the longest first.
+struct QueryPass {
+  unsigned works;
+  int tiles;
+  Divisor group, kv_heads, batch;
+};
+struct QueryWork {
+  int b, kvh, qrow, t0, len, n;  // n = 0: nothing to do
+  KeyTiles kt;
+};
+__device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const QueryPass& qp, unsigned x) {
+  unsigned g, kvh, b;
+  x = qp.group.div(x, g);
+  x = qp.kv_heads.div(x, kvh);
+  x = qp.batch.div(x, b);
+  QueryWork w;
+  w.b = b, w.kvh = kvh, w.qrow = b * p.H + kvh * qp.group.d + g;
+  w.t0 = (qp.tiles - 1 - static_cast<int>(x)) * kT;
+  w.len = window::seq_len(p, b);
+  w.kt = window::key_tiles<kT>(w.t0, min(w.t0 + kT, w.len) - 1, p.window, p.n_sink);
+  w.n = w.t0 < w.len ? w.kt.count() : 0;
+  return w;
+}
+// The r-th work of this CTA: every other round runs backwards, so that long and short works meet.
+__device__ __forceinline__ unsigned nth_work(unsigned r) {
+  return r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     window_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, WindowArgs p,
-                        const float2* rows) {
+                        const float2* rows, QueryPass qp) {
   using S = Smem<D>;
   constexpr int kNP = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready, done;
+  __shared__ uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready[2], done, last;
   __shared__ uint32_t tmem_base;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT;
-  unsigned x = blockIdx.x;  // (sequence, k/v head, query tiles from the last down, heads of the group)
-  const int g = x % G;
-  x /= G;
-  const int qt = tiles - 1 - static_cast<int>(x % tiles);
-  x /= tiles;
-  const int kvh = x % p.Hkv, b = x / p.Hkv;
-  const int len = window::seq_len(p, b), t0 = qt * kT;
-  if (t0 >= len) return;
-  const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kT, len) - 1, p.window, p.n_sink);
-  const int n = kt.count(), qrow = b * p.H + kvh * G + g;
-
   if (tid == 0) {
-    sm100::mbar_init(&q_full, 1);
+    sm100::mbar_init(&q_full, 1), sm100::mbar_init(&q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&k_full[i], 1), sm100::mbar_init(&k_empty[i], 1);
       sm100::mbar_init(&v_full[i], 1), sm100::mbar_init(&v_empty[i], 1);
+      sm100::mbar_init(&dp_ready[i], 1), sm100::mbar_init(&ds_ready[i], 8);
     }
     sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&s_free, 8);
-    sm100::mbar_init(&dp_ready[0], 1), sm100::mbar_init(&dp_ready[1], 1), sm100::mbar_init(&ds_ready, 8);
-    sm100::mbar_init(&done, 1);
+    sm100::mbar_init(&done, 1), sm100::mbar_init(&last, 1);
     sm100::fence_mbar_init();
   }
   if (warp == 9) {
@@ -407,144 +435,183 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------------------------------ loads
     if (lane == 0) {
-      sm100::prefetch_tmap(&tm_k), sm100::prefetch_tmap(&tm_v);
-      sm100::mbar_arrive_expect_tx(&q_full, 2 * S::kTile);
-      load_tile<kNP>(sm + S::kFixed, &tm_q, &q_full, t0, qrow);
-      load_tile<kNP>(sm + S::kFixed + S::kTile, &tm_do, &q_full, t0, qrow);
-      int it = 0;
-      bool k_sent = false;
-      for (; it < n; ++it) {
-        const int slot = it & 1, round = it >> 1, j0 = kt.walk(it) * kT, row = b * p.Hkv + kvh;
-        k_sent = false;
-        if (round > 0) fine = sm100::mbar_wait_bounded(&k_empty[slot], (round - 1) & 1, kWaitCycles);
-        if (!fine) break;
-        sm100::mbar_arrive_expect_tx(&k_full[slot], S::kTile);
-        load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_k, &k_full[slot], j0, row);
-        k_sent = true;
-        if (round > 0) fine = sm100::mbar_wait_bounded(&v_empty[slot], (round - 1) & 1, kWaitCycles);
-        if (!fine) break;
-        sm100::mbar_arrive_expect_tx(&v_full[slot], S::kTile);
-        load_tile<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, &tm_v, &v_full[slot], j0, row);
+      sm100::prefetch_tmap(&tm_q), sm100::prefetch_tmap(&tm_do), sm100::prefetch_tmap(&tm_k), sm100::prefetch_tmap(&tm_v);
+      unsigned nq = 0, nk = 0, nv = 0;  // copies issued so far
+      for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
+        const unsigned x = nth_work(r);
+        if (x >= qp.works) continue;
+        const QueryWork w = query_work(p, qp, x);
+        const int row = w.b * p.Hkv + w.kvh;
+        for (int it = 0; it < w.n; ++it) {
+          const unsigned slot = nk & 1;
+          const int j0 = w.kt.walk(it) * kT;
+          if (nk > 1) fine = sm100::mbar_wait_bounded(&k_empty[slot], ((nk >> 1) - 1) & 1, kWaitCycles);
+          if (!fine) break;
+          sm100::mbar_arrive_expect_tx(&k_full[slot], S::kTile);
+          load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_k, &k_full[slot], j0, row);
+          ++nk;
+          if (nv > 1) fine = sm100::mbar_wait_bounded(&v_empty[slot], ((nv >> 1) - 1) & 1, kWaitCycles);
+          if (!fine) break;
+          sm100::mbar_arrive_expect_tx(&v_full[slot], S::kTile);
+          load_tile<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, &tm_v, &v_full[slot], j0, row);
+          ++nv;
+          if (it == 0) {
+            if (nq > 0) fine = sm100::mbar_wait_bounded(&q_empty, (nq - 1) & 1, kWaitCycles);
+            if (!fine) break;
+            sm100::mbar_arrive_expect_tx(&q_full, 2 * S::kTile);
+            load_tile<kNP>(sm + S::kFixed, &tm_q, &q_full, w.t0, w.qrow);
+            load_tile<kNP>(sm + S::kFixed + S::kTile, &tm_do, &q_full, w.t0, w.qrow);
+            ++nq;
+          }
+        }
       }
       if (!fine) {  // nothing of this CTA may be in flight when it ends
-        sm100::mbar_wait_bounded(&q_full, 0, kWaitCycles);
-        for (int back = it > 1 ? it - 1 : 0; back <= it && back < n; ++back) {
-          if (back < it || k_sent) sm100::mbar_wait_bounded(&k_full[back & 1], (back >> 1) & 1, kWaitCycles);
-          if (back < it) sm100::mbar_wait_bounded(&v_full[back & 1], (back >> 1) & 1, kWaitCycles);
-        }
+        if (nq > 0) sm100::mbar_wait_bounded(&q_full, (nq - 1) & 1, kWaitCycles);
+        for (unsigned c = nk > 2 ? nk - 2 : 0; c < nk; ++c) sm100::mbar_wait_bounded(&k_full[c & 1], (c >> 1) & 1, kWaitCycles);
+        for (unsigned c = nv > 2 ? nv - 2 : 0; c < nv; ++c) sm100::mbar_wait_bounded(&v_full[c & 1], (c >> 1) & 1, kWaitCycles);
       }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------------------ products
-    const uint32_t q_addr = sm100::smem_u32(sm + S::kFixed), do_addr = q_addr + S::kTile;
     const uint32_t ring = sm100::smem_u32(sm + S::kRing);
-    // S and dP of tile ``it``; k and v rows behind the end are zeroed (their weights are zero)
-    auto issue = [&](int it) {
-      const int slot = it & 1, inside = len - kt.walk(it) * kT;
-      if (inside < kT) {
-        zero_rows<kNP>(sm + S::kRing + 2 * slot * S::kTile, inside, lane);
-        zero_rows<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, inside, lane);
-      }
-      if (lane == 0) {
-        mma_rows<D>(t_s, rows_desc(q_addr), rows_desc(ring + 2 * slot * S::kTile));
-        sm100::mma_commit(&s_ready);
-        mma_rows<D>(t_dp + 128 * slot, rows_desc(do_addr), rows_desc(ring + (2 * slot + 1) * S::kTile));
-        sm100::mma_commit(&dp_ready[slot]);
-        sm100::mma_commit(&v_empty[slot]);
-      }
-    };
-    fine = warp_wait(&q_full, 0) && warp_wait(&k_full[0], 0) && warp_wait(&v_full[0], 0);
-    if (fine) issue(0);
-    for (int it = 0; it < n && fine; ++it) {
-      const int slot = it & 1, next = (it + 1) & 1, next_round = (it + 1) >> 1;
-      if (it + 1 < n) {
-        fine = warp_wait(&k_full[next], next_round & 1) && warp_wait(&v_full[next], next_round & 1) && warp_wait(&s_free, it & 1);
+    const uint64_t q_desc = rows_desc(sm100::smem_u32(sm + S::kFixed)), do_desc = rows_desc(sm100::smem_u32(sm + S::kFixed + S::kTile));
+    unsigned c = 0, nq = 0;  // key tiles and works begun
+    for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
+      const unsigned x = nth_work(r);
+      if (x >= qp.works) continue;
+      const QueryWork w = query_work(p, qp, x);
+      if (w.n == 0) continue;
+      // S and dP of the it-th tile, the c-th of this CTA: S is free once tile c - 1 is in registers.  k and v rows behind
+      // the end are zeroed (their weights are zero).
+      auto issue = [&](int it) {
+        const unsigned slot = c & 1;
+        fine = warp_wait(&k_full[slot], (c >> 1) & 1) && warp_wait(&v_full[slot], (c >> 1) & 1) &&
+               (c == 0 || warp_wait(&s_free, (c - 1) & 1));
+        if (!fine) return;
+        sm100::tc_fence_after();
+        const int inside = w.len - w.kt.walk(it) * kT;
+        if (inside < kT) {
+          zero_rows<kNP>(sm + S::kRing + 2 * slot * S::kTile, inside, lane);
+          zero_rows<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, inside, lane);
+        }
+        if (lane == 0) {
+          const uint64_t k_desc = rows_desc(ring + 2 * slot * S::kTile);
+          mma_rows<D>(t_s, q_desc, k_desc);
+          sm100::mma_commit(&s_ready);
+          mma_rows<D>(t_dp + 128 * slot, do_desc, k_desc + (S::kTile >> 4));
+          sm100::mma_commit(&dp_ready[slot]);
+          sm100::mma_commit(&v_empty[slot]);
+          if (it + 1 == w.n) sm100::mma_commit(&q_empty);
+        }
+        ++c;
+      };
+      fine = warp_wait(&q_full, nq & 1);
+      ++nq;
+      if (fine) issue(0);
+      for (int it = 0; it < w.n && fine; ++it) {
+        const unsigned mine = c - 1, slot = mine & 1;  // tile ``it``
+        if (it + 1 < w.n) issue(it + 1);
+        if (!fine) break;
+        fine = warp_wait(&ds_ready[slot], (mine >> 1) & 1);
         if (!fine) break;
         sm100::tc_fence_after();
-        issue(it + 1);
-      }
-      fine = warp_wait(&ds_ready, it & 1);
-      if (!fine) break;
-      sm100::tc_fence_after();
-      if (lane == 0) {
-        mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring + 2 * slot * S::kTile), it > 0);
-        sm100::mma_commit(&k_empty[slot]);
+        if (lane == 0) {
+          mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring + 2 * slot * S::kTile), it > 0);
+          sm100::mma_commit(&k_empty[slot]);
+          if (it + 1 == w.n) sm100::mma_commit(&done);
+        }
       }
     }
-    if (lane == 0) {
-      sm100::mma_commit(&done);
-      if (!fine) sm100::mbar_wait_bounded(&done, 0, kWaitCycles);
+    if (!fine && lane == 0) {  // the products in flight read shared memory and write TMEM
+      sm100::mma_commit(&last);
+      sm100::mbar_wait_bounded(&last, 0, kWaitCycles);
     }
   } else {
     // ------------------------------------------------------------------------------------ weights
-    const int half = warp >> 2, t = t0 + (tid & 127);
+    const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const float c = p.scale * kLog2e;
-    const int w_first = t0 + 32 * (warp & 3), w_last = w_first + 31;
-    const float2 r = t < len ? rows[(size_t)qrow * p.L + t] : make_float2(0.f, 0.f);
-    for (int it = 0; it < n; ++it) {
-      const int j0 = kt.walk(it) * kT + 64 * half;
-      fine = warp_wait(&s_ready, it & 1);
-      if (!fine) break;
-      sm100::tc_fence_after();
-      float s[2][32];
-      sm100::tmem_ld32(t_s + lanes + 64 * half, s[0]);
-      sm100::tmem_ld32(t_s + lanes + 64 * half + 32, s[1]);
-      sm100::tmem_wait_ld();
-      sm100::tc_fence_before();
-      warp_arrive(&s_free);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[u][e] = exp2_fast(fmaf(s[u][e], c, -r.x));
-      const bool all_seen = j0 + 63 <= w_first && (w_last - j0 < p.window || j0 + 64 <= p.n_sink);
-      if (!all_seen) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {  // 32 keys: all of the warp's rows see them, or some do
-          const int k0 = j0 + 32 * u;
-          if (k0 + 31 <= w_first && (w_last - k0 < p.window || k0 + 32 <= p.n_sink)) continue;
-          const int hi = t - k0, lo = hi - p.window, sinks = p.n_sink - k0;
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e > hi || (e <= lo && e >= sinks)) s[u][e] = 0.f;
-        }
-      }
-      fine = warp_wait(&dp_ready[it & 1], (it >> 1) & 1);
-      if (!fine) break;
-      sm100::tc_fence_after();
-      const uint32_t t_mine = t_dp + 128 * (it & 1) + lanes + 64 * half;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float dp[32], w[16];
-        sm100::tmem_ld32(t_mine + 32 * u, dp);
+    const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
+    const bool wide = is_wide(p.dq);
+    unsigned c = 0, works = 0;
+    for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
+      const unsigned x = nth_work(r);
+      if (x >= qp.works) continue;
+      const QueryWork w = query_work(p, qp, x);
+      if (w.n == 0) continue;
+      const int t = w.t0 + (tid & 127);
+      const int w_first = w.t0 + 32 * (warp & 3), w_last = w_first + 31;
+      const float2 row = t < w.len ? rows[(size_t)w.qrow * p.L + t] : make_float2(0.f, 0.f);
+      const float2 l2 = make_float2(row.x, row.x), d2 = make_float2(row.y, row.y);
+      for (int it = 0; it < w.n; ++it, ++c) {
+        const int j0 = w.kt.walk(it) * kT + 64 * half;
+        fine = warp_wait(&s_ready, c & 1);
+        if (!fine) break;
+        sm100::tc_fence_after();
+        float s[2][32];
+        sm100::tmem_ld32(t_s + lanes + 64 * half, s[0]);
+        sm100::tmem_ld32(t_s + lanes + 64 * half + 32, s[1]);
         sm100::tmem_wait_ld();
+        sm100::tc_fence_before();
+        warp_arrive(&s_free);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = __uint_as_float(pack_bf16(s[u][2 * e] * (dp[2 * e] - r.y), s[u][2 * e + 1] * (dp[2 * e + 1] - r.y)));
-        sm100::tmem_st16(t_mine + 16 * u, w);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = fma2(make_float2(s[u][e], s[u][e + 1]), c2, l2);
+            s[u][e] = exp2_fast(y.x), s[u][e + 1] = exp2_fast(y.y);
+          }
+        const bool all_seen = j0 + 63 <= w_first && (w_last - j0 < p.window || j0 + 64 <= p.n_sink);
+        if (!all_seen) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {  // 32 keys: all of the warp's rows see them, or some do
+            const int k0 = j0 + 32 * u;
+            if (k0 + 31 <= w_first && (w_last - k0 < p.window || k0 + 32 <= p.n_sink)) continue;
+            const int hi = t - k0, lo = hi - p.window, sinks = p.n_sink - k0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e > hi || (e <= lo && e >= sinks)) s[u][e] = 0.f;
+          }
+        }
+        fine = warp_wait(&dp_ready[c & 1], (c >> 1) & 1);
+        if (!fine) break;
+        sm100::tc_fence_after();
+        const uint32_t t_mine = t_dp + 128 * (c & 1) + lanes + 64 * half;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float dp[32], q[16];
+          sm100::tmem_ld32(t_mine + 32 * u, dp);
+          sm100::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = mul2(make_float2(s[u][e], s[u][e + 1]), add2(make_float2(dp[e], dp[e + 1]), d2));
+            q[e / 2] = __uint_as_float(pack_bf16(y.x, y.y));
+          }
+          sm100::tmem_st16(t_mine + 16 * u, q);
+        }
+        sm100::tmem_wait_st();
+        sm100::tc_fence_before();
+        warp_arrive(&ds_ready[c & 1]);
       }
-      sm100::tmem_wait_st();
-      sm100::tc_fence_before();
-      warp_arrive(&ds_ready);
-    }
-    if (fine) {
-      fine = warp_wait(&done, 0);
-      sm100::tc_fence_after();
-    }
-    if (fine) {  // each half writes half of the columns
-      const bool wide = is_wide(p.dq);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq) + ((size_t)qrow * p.L + t) * D + half * (D / 2);
+      if (fine) {
+        fine = warp_wait(&done, works & 1);
+        ++works;
+        sm100::tc_fence_after();
+      }
+      if (!fine) break;
+      // each half writes half of the columns
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq) + ((size_t)w.qrow * p.L + t) * D + half * (D / 2);
 #pragma unroll 1
       for (int u = 0; u < D / 2; u += 32) {
         float a[32];
         sm100::tmem_ld32(t_dq + lanes + half * (D / 2) + u, a);
         sm100::tmem_wait_ld();
-        if (t < len) {
+        if (t < w.len) {
 #pragma unroll
           for (int e = 0; e < 32; e += 16) store32(out + u + e, pack8_bf16(a + e, p.scale), pack8_bf16(a + e + 8, p.scale), wide);
         }
         __syncwarp();
       }
+      sm100::tc_fence_before();  // dq is read: the next work's first product follows this warp's next arrival
     }
   }
   if (!fine) raise_status(p.status, kStatusTimeout);
@@ -596,10 +663,13 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
       !make_bf16_tmap_rows(&td, p.out_dtype == kBF16 ? p.dO : dO16, p.B * p.H, p.L, D, kT))
     return cudaErrorInvalidValue;
   const size_t tokens = (size_t)p.B * p.H * p.L;
-  window_rows_kernel<D><<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(p, rows, dO16);
+  window_rows_kernel<D><<<(unsigned)((tokens * (D / 8) + 255) / 256), 256, 0, stream>>>(p, rows, dO16);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int smem = Smem<D>::kTotal + 1024, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return cudaErrorInvalidDevice;
   e = cudaFuncSetAttribute(window_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(window_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -608,7 +678,10 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, kp);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  window_dq_tc_kernel<D><<<(unsigned)((long long)p.B * p.H * tiles), kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows);
+  QueryPass qp;
+  qp.works = (unsigned)((long long)p.B * p.H * tiles), qp.tiles = tiles;
+  qp.group = make_divisor(p.H / p.Hkv), qp.kv_heads = make_divisor(p.Hkv), qp.batch = make_divisor(p.B);
+  window_dq_tc_kernel<D><<<qp.works < (unsigned)sms ? qp.works : (unsigned)sms, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, qp);
   e = cudaGetLastError();
   if (e != cudaSuccess || kp.sinks == 0) return e;
   const size_t words = (size_t)bh * kp.sinks * 2 * kT * D / 8;
