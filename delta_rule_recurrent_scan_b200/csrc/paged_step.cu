@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThr) paged_step_kernel(PagedStepArgs p) {
   __shared__ float keep_s[kHB], l_s[kHB], m_s[kHB];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Part w = which<kHB>(p);
+  if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int r = p.row ? p.row[w.b] : w.b;
   int n = 0;
   const int* entries = nullptr;
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepA
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const Part w = which<kMHB>(p);
+  if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int r = p.row ? p.row[w.b] : w.b;
   int n = 0;
   const int* entries = nullptr;
@@ -262,6 +264,18 @@ __global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepA
       const int j0 = kt.walk(u) * kMT;
       const uint32_t dst = stage0 + stage * 2 * Sm::kTile;
       const bool full = j0 + kMT <= n && (n - 1 - j0 < win || j0 + kMT <= p.n_sink);
+      if (full && one_page) {  // one page, every token: the addresses differ by constants
+        const bool there = entry >= 0 && entry < p.num_pages;
+        bad |= !there;
+        const size_t at = there ? ((((size_t)entry * p.Hkv + w.kvh) << shift) + (j0 & mask) + row0) * D + 8 * chunk : 0;
+#pragma unroll
+        for (int i = 0; i < kMT / kRows; ++i) {
+          const int row = row0 + i * kRows;
+          const uint32_t to = dst + row * (D * 2) + ((chunk ^ (row & 7)) << 4);
+          copy16_or_zero(to, kp + at + i * kRows * D, there);
+          copy16_or_zero(to + Sm::kTile, vp + at + i * kRows * D, there);
+        }
+      } else {
 #pragma unroll
       for (int i = 0; i < kMT / kRows; ++i) {
         const int row = row0 + i * kRows, j = j0 + row;
@@ -272,6 +286,7 @@ __global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepA
         const uint32_t to = dst + row * (D * 2) + ((chunk ^ (row & 7)) << 4);
         copy16_or_zero(to, kp + at, there);
         copy16_or_zero(to + Sm::kTile, vp + at, there);
+      }
       }
     }
     async_commit();
@@ -316,15 +331,19 @@ __global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepA
       entry = next;
     }
     const uint32_t k_at = stage0 + stage * 2 * Sm::kTile, v_at = k_at + Sm::kTile;
-    float s[2][4] = {};
+    float s[2][4] = {}, s2[2][4] = {};  // two chains of products each
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const int row = ((lane >> 4) << 3) + (lane & 7), c = 2 * ks + ((lane >> 3) & 1);
       uint32_t b[4];
       ldsm4(b, k_at + row * (D * 2) + ((c ^ (row & 7)) << 4));
-      mma16816(s[0], q[ks], b[0], b[1]);
-      mma16816(s[1], q[ks], b[2], b[3]);
+      mma16816(ks & 1 ? s2[0] : s[0], q[ks], b[0], b[1]);
+      mma16816(ks & 1 ? s2[1] : s[1], q[ks], b[2], b[3]);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] += s2[i][e];
     const int j0 = kt.walk(u) * kMT;
     if (!(j0 + kMT <= n && (n - 1 - j0 < win || j0 + kMT <= p.n_sink))) {
 #pragma unroll
@@ -417,25 +436,70 @@ __global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepA
   }
 }
 
-// Joins a head's parts: one CTA of d_v threads (at least a warp) per head.
+// Joins a head's parts: one CTA per head.  The parts' factors exp(m_i - M) are made once, in shared memory; then 256 / (d_v / 4)
+// groups of threads add every group-th part, four columns a thread, and the groups are added in order.
+constexpr int kJoin = 256, kMaxParts = 1024;
 template <int DV>
-__global__ void __launch_bounds__(DV < 32 ? 32 : DV) paged_join_kernel(PagedStepArgs p) {
+__global__ void __launch_bounds__(kJoin) paged_join_kernel(PagedStepArgs p) {
+  constexpr int kCols = DV / 4, kGroups = kJoin / kCols;
+  __shared__ float f_s[kMaxParts], red[8];
+  __shared__ __align__(16) float4 o_s[kJoin];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t head = blockIdx.x;
   const float* pm = part_max(p, DV) + head * p.splits;
   const float* pl = part_sum(p, DV) + head * p.splits;
-  const float* po = p.part + head * p.splits * DV;
+  const float4* po = reinterpret_cast<const float4*>(p.part + head * p.splits * DV);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are still being made
   float M = -INFINITY;
-  for (int i = 0; i < p.splits; ++i) M = fmaxf(M, pm[i]);
+  for (int i = tid; i < p.splits; i += kJoin) M = fmaxf(M, pm[i]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoin / 32; ++i) M = fmaxf(M, red[i]);
+  __syncthreads();
   const float base = M == -INFINITY ? 0.f : M;
-  float l = 0.f, x = 0.f;
-  const int col = threadIdx.x;
-  for (int i = 0; i < p.splits; ++i) {
+  float l = 0.f;
+  for (int i = tid; i < p.splits; i += kJoin) {
     const float f = expf(pm[i] - base);
+    f_s[i] = f;
     l = fmaf(f, pl[i], l);
-    if (col < DV) x = fmaf(f, po[(size_t)i * DV + col], x);
   }
-  if (col < DV) store_elem(p.o, head * DV + col, l == 0.f ? 0.f : x / l, p.out_dtype);
-  if (col == 0 && p.lse) p.lse[head] = M + logf(l);
+  l = warp_sum(l);
+  if (lane == 0) red[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoin / 32; ++i) l += red[i];
+  const int col = tid % kCols, group = tid / kCols;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = group; i < p.splits; i += kGroups) {
+    const float4 v = po[(size_t)i * kCols + col];
+    const float f = f_s[i];
+    a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
+  }
+  o_s[tid] = a;
+  __syncthreads();
+  if (tid < DV) {
+    float x = 0.f;
+    for (int g = 0; g < kGroups; ++g) x += reinterpret_cast<const float*>(o_s)[g * DV + tid];
+    store_elem(p.o, head * DV + tid, l == 0.f ? 0.f : x / l, p.out_dtype);
+    if (tid == 0 && p.lse) p.lse[head] = M + logf(l);
+  }
+}
+
+// The join's launch overlaps the end of the kernel before it (its wait is at its top).
+template <int DV>
+cudaError_t join(const PagedStepArgs& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n * p.H), cfg.blockDim = dim3(kJoin), cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, p);
 }
 
 template <int DK, int DV>
@@ -445,8 +509,7 @@ cudaError_t step(const PagedStepArgs& p, cudaStream_t stream) {
   paged_step_kernel<DK, DV><<<(unsigned)ctas, kThr, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  paged_join_kernel<DV><<<p.n * p.H, DV < 32 ? 32 : DV, 0, stream>>>(p);
-  return cudaGetLastError();
+  return join<DV>(p, stream);
 }
 
 bool step_mma_supported(int dk, int dv, int in_dtype) { return in_dtype == kBF16 && dk == dv && (dk == 64 || dk == 128); }
@@ -463,8 +526,7 @@ cudaError_t step_mma(const PagedStepArgs& p, cudaStream_t stream) {
   kernel<<<(unsigned)ctas, 32 * kMWarps, StepSmem<D>::kTotal, stream>>>(p, shift);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
-  paged_join_kernel<D><<<p.n * p.H, D, 0, stream>>>(p);
-  return cudaGetLastError();
+  return join<D>(p, stream);
 }
 
 template <typename F>
@@ -495,6 +557,7 @@ int paged_step_splits(int dk, int dv, int in_dtype, int n, int H, int Hkv, long 
     s = (4 * 148 + pairs - 1) / pairs;
     if (s > tiles / 4) s = tiles / 4;
   }
+  if (s > kMaxParts) s = kMaxParts;
   return s < 1 ? 1 : (int)s;
 }
 
