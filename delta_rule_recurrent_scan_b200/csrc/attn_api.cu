@@ -121,7 +121,7 @@ size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int window
 }
 
 kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
-                           const int* lens, int window, int n_sink, float scale, void* o, float* lse, void* workspace,
+                           const int* lens, int zero_rest, int window, int n_sink, float scale, void* o, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream) {
   KDN_TRY(window_checks(dims, kv_heads, window, n_sink, scale));
   const bool none = dims->L == 0;
@@ -139,7 +139,7 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
   if (workspace != nullptr) KDN_TRY(clear_status(workspace, st));
   if (none) return ok();
   kdn::WindowArgs a{};
-  a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens;
+  a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens, a.zero_rest = zero_rest != 0;
   a.B = dims->B, a.H = dims->H, a.Hkv = kv_heads, a.L = dims->L, a.scale = scale;
   a.window = window < dims->L ? window : dims->L, a.n_sink = n_sink < dims->L ? n_sink : dims->L;  // t - j < L
   a.o = o, a.lse = lse, a.status = static_cast<unsigned*>(workspace);
@@ -147,7 +147,7 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
 }
 
 kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
-                                    const int* lens, int window, int n_sink, float scale, const void* o,
+                                    const int* lens, int zero_rest, int window, int n_sink, float scale, const void* o,
                                     const float* lse, const void* dO, void* dq, void* dk, void* dv, void* workspace,
                                     size_t workspace_bytes, void* stream) {
   KDN_TRY(window_checks(dims, kv_heads, window, n_sink, scale));
@@ -168,7 +168,7 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
   cudaStream_t st = (cudaStream_t)stream;
   if (none) return clear_status(workspace, st);
   kdn::WindowArgs a{};
-  a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens;
+  a.q = q, a.k = k, a.v = v, a.in_dtype = dims->in_dtype, a.out_dtype = dims->out_dtype, a.lens = lens, a.zero_rest = zero_rest != 0;
   a.B = dims->B, a.H = dims->H, a.Hkv = kv_heads, a.L = dims->L, a.scale = scale;
   a.window = window < dims->L ? window : dims->L, a.n_sink = n_sink < dims->L ? n_sink : dims->L;  // t - j < L
   a.o = const_cast<void*>(o), a.lse = const_cast<float*>(lse), a.status = static_cast<unsigned*>(workspace);

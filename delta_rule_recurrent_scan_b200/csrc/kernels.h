@@ -261,6 +261,7 @@ struct WindowArgs {
   int in_dtype;
   int out_dtype;        // of o and dO
   const int* lens;      // [B] tokens per sequence, or nullptr (L)
+  bool zero_rest;       // rows behind a sequence's end: set to zero, or left as they were
   int B, H, Hkv, L;
   int window;           // >= 1
   int n_sink;           // >= 0

@@ -49,6 +49,7 @@ __device__ __forceinline__ void stage(float* dst, const void* src, size_t row0, 
 template <int D>
 __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, int ra, const float* b, int rb) {
   constexpr int S = D + 4;
+  float2 sum[4][4] = {};  // even and odd coordinates
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
     float4 x[4], y[4];
@@ -60,7 +61,27 @@ __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, int
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[i][j] = fmaf(x[i].w, y[j].w, fmaf(x[i].z, y[j].z, fmaf(x[i].y, y[j].y, fmaf(x[i].x, y[j].x, acc[i][j]))));
+        sum[i][j] = window::fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w),
+                                 window::fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] += sum[i][j].x + sum[i][j].y;
+}
+
+// a[n] += w b[n], two at a time.
+template <int N>
+__device__ __forceinline__ void axpy(float (&a)[N], float w, const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int n = 0; n < N; n += 2) {
+      const float2 r = window::fma2(make_float2(w, w), make_float2(b[n], b[n + 1]), make_float2(a[n], a[n + 1]));
+      a[n] = r.x, a[n + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n) a[n] = fmaf(w, b[n], a[n]);
   }
 }
 
@@ -98,9 +119,7 @@ __device__ __forceinline__ void rows_times_tile(float (&acc)[4][D / 16], const f
       row_vals<D>(x, b + (j + u) * (D + 4), tx);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float pw = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) acc[i][n] = fmaf(pw, x[n], acc[i][n]);
+        axpy(acc[i], u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w, x);
       }
     }
   }
@@ -114,13 +133,7 @@ __device__ __forceinline__ void cols_times_tile(float (&acc)[4][D / 16], const f
     const float4 p = *reinterpret_cast<const float4*>(w + t * kLP + 4 * ty);
     float x[D / 16];
     row_vals<D>(x, b + t * (D + 4), tx);
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) {
-      acc[0][n] = fmaf(p.x, x[n], acc[0][n]);
-      acc[1][n] = fmaf(p.y, x[n], acc[1][n]);
-      acc[2][n] = fmaf(p.z, x[n], acc[2][n]);
-      acc[3][n] = fmaf(p.w, x[n], acc[3][n]);
-    }
+    axpy(acc[0], p.x, x), axpy(acc[1], p.y, x), axpy(acc[2], p.z, x), axpy(acc[3], p.w, x);
   }
 }
 
@@ -129,6 +142,14 @@ template <int D>
 __device__ __forceinline__ void put_row(void* dst, size_t row, const float (&x)[D / 16], float f, int tx, int dtype) {
 #pragma unroll
   for (int n = 0; n < D / 16; ++n) store_elem(dst, row * D + col_of<D>(tx, n), x[n] * f, dtype);
+}
+
+// Rows t .. t0 + 63 (t = the sequence's end, or t0 where the tile lies behind it) of a [L, D] array become zero.
+template <int D>
+__device__ __forceinline__ void zero_tile(void* dst, size_t row0, int t0, int len, int L, int dtype) {
+  const int first = max(t0, len), last = min(t0 + kT, L), words = D * (dtype == kBF16 ? 2 : 4) / 16;
+  for (int e = threadIdx.x; e < (last - first) * words; e += kThreads)
+    static_cast<uint4*>(dst)[(row0 + first) * words + e] = make_uint4(0, 0, 0, 0);
 }
 
 // Which tile, head and sequence this CTA has: tiles run fastest from the last one down (it has the longest walk).
@@ -154,8 +175,13 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WindowArgs p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Where w = where((p.L + kT - 1) / kT, p.H);
   const int len = window::seq_len(p, w.b), t0 = w.tile * kT;
-  if (t0 >= len) return;
   const size_t qrow = ((size_t)w.b * p.H + w.h) * p.L;
+  if (p.zero_rest && t0 + kT > len) {
+    zero_tile<DV>(p.o, qrow, t0, len, p.L, p.out_dtype);
+    const int t = max(t0, len) + tid;
+    if (t < min(t0 + kT, p.L)) p.lse[qrow + t] = 0.f;
+  }
+  if (t0 >= len) return;
   const size_t krow = ((size_t)w.b * p.Hkv + w.h / (p.H / p.Hkv)) * p.L;
   const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kT, len) - 1, p.window, p.n_sink);
   stage<DK>(q_s, p.q, qrow, t0, len, p.in_dtype);
@@ -273,8 +299,9 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Where w = where((p.L + kT - 1) / kT, p.H);
   const int len = window::seq_len(p, w.b), t0 = w.tile * kT;
-  if (t0 >= len) return;
   const size_t qrow = ((size_t)w.b * p.H + w.h) * p.L;
+  if (p.zero_rest && t0 + kT > len) zero_tile<DK>(p.dq, qrow, t0, len, p.L, p.in_dtype);
+  if (t0 >= len) return;
   const size_t krow = ((size_t)w.b * p.Hkv + w.h / (p.H / p.Hkv)) * p.L;
   const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kT, len) - 1, p.window, p.n_sink);
   stage<DK>(q_s, p.q, qrow, t0, len, p.in_dtype);
@@ -320,9 +347,13 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_kernel(WindowArgs p) {
   Where w = where((p.L + kT - 1) / kT, p.Hkv);
   w.tile = (p.L + kT - 1) / kT - 1 - w.tile;  // the first tiles (sinks) have the longest walk
   const int len = window::seq_len(p, w.b), j0 = w.tile * kT;
-  if (j0 >= len) return;
   const int G = p.H / p.Hkv;
   const size_t krow = ((size_t)w.b * p.Hkv + w.h) * p.L;
+  if (p.zero_rest && j0 + kT > len) {
+    zero_tile<DK>(p.dk, krow, j0, len, p.L, p.in_dtype);
+    zero_tile<DV>(p.dv, krow, j0, len, p.L, p.in_dtype);
+  }
+  if (j0 >= len) return;
   int lo, hi;
   window::query_tiles<kT>(j0, min(j0 + kT, len) - 1, len, p.window, p.n_sink, lo, hi);
   stage<DK>(k_s, p.k, krow, j0, len, p.in_dtype);

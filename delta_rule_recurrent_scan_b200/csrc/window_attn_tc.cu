@@ -244,8 +244,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const unsigned x = r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         if (x >= sch.works) continue;
       const Work w = make_work(p, sch, x);
-      if (w.n == 0 || (i == 1 && !w.two)) continue;
       const int t0 = (i == 0 ? w.qt[0] : w.qt[1]) * kT, t = t0 + row;
+      const size_t head = (size_t)w.b * p.H + (i == 0 ? w.h[0] : w.h[1]);
+      if (p.zero_rest && t0 + kT > w.len) {
+        zero_tile(p.o, head * p.L, D * (p.out_dtype == kBF16 ? 2 : 4), t0, w.len, p.L, row, 128);
+        if (t >= w.len && t < p.L) p.lse[head * p.L + t] = 0.f;
+      }
+      if (w.n == 0 || (i == 1 && !w.two)) continue;
       const int w_first = t0 + 32 * (warp & 3), w_last = w_first + 31;  // the warp's rows
       float m = -INFINITY, l = 0.f;
       for (int it = 0; it < w.n; ++it) {
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sm100::tc_fence_before();
         warp_arrive(&p_ready[i]);
       }
-      const size_t at = ((size_t)w.b * p.H + (i == 0 ? w.h[0] : w.h[1])) * p.L + t;
+      const size_t at = head * p.L + t;
       if (fine) {
         fine = warp_wait(&done[i], done_phase);
         done_phase ^= 1;

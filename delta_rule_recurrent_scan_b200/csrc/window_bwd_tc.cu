@@ -116,6 +116,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   const int kvh = y % p.Hkv, b = y / p.Hkv;
   const int len = window::seq_len(p, b), j0 = tile * kT;
+  if (p.zero_rest && part == 0 && j0 + kT > len) {
+    const size_t row0 = (size_t)(b * p.Hkv + kvh) * p.L;
+    zero_tile(p.dk, row0, 2 * D, j0, len, p.L, tid, kTcThreads);
+    zero_tile(p.dv, row0, 2 * D, j0, len, p.L, tid, kTcThreads);
+  }
   if (j0 >= len) return;
   int lo, hi;
   window::query_tiles<kT>(j0, min(j0 + kT, len) - 1, len, p.window, p.n_sink, lo, hi);
@@ -537,6 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const unsigned x = nth_work(r);
       if (x >= qp.works) continue;
       const QueryWork w = query_work(p, qp, x);
+      if (p.zero_rest && w.t0 + kT > w.len) zero_tile(p.dq, (size_t)w.qrow * p.L, 2 * D, w.t0, w.len, p.L, tid, 256);
       if (w.n == 0) continue;
       const int t = w.t0 + (tid & 127);
       const int w_first = w.t0 + 32 * (warp & 3), w_last = w_first + 31;

@@ -35,6 +35,13 @@ __device__ __forceinline__ uint4 pack8_bf16(const float* x, float f) {
                     pack_bf16(x[6] * f, x[7] * f));
 }
 
+// Rows max(t0, len) .. t0 + 127 of a [.., L, D] array become zero (bytes per row a multiple of 16), by ``threads`` threads.
+__device__ __forceinline__ void zero_tile(void* dst, size_t row0, int row_bytes, int t0, int len, int L, int tid, int threads) {
+  const int first = max(t0, len), last = min(t0 + kT, L), words = row_bytes / 16;
+  for (int e = tid; e < (last - first) * words; e += threads)
+    static_cast<uint4*>(dst)[(row0 + first) * words + e] = make_uint4(0, 0, 0, 0);
+}
+
 // One arrival for a warp, after all its lanes' work (32 single arrivals on one word take turns).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -51,28 +58,6 @@ __device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b,
   }
 }
 __device__ __forceinline__ bool is_wide(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 
 // Division by a number known at launch: q = floor(x / d) for x < 2^31 (multiply by ceil(2^(32 + s) / d), s = ceil(log2 d)).
 struct Divisor {

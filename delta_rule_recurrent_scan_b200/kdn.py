@@ -107,8 +107,8 @@ def lib() -> ctypes.CDLL:
                            ctypes.POINTER(ctypes.c_char_p)]
     L.kdn_plan.restype = ctypes.c_int
     pages = ctypes.POINTER(PagesC)
-    L.kdn_window_attn.argtypes = [dims, i, vp, vp, vp, vp, i, i, f, vp, vp, vp, sz, vp]
-    L.kdn_window_attn_backward.argtypes = [dims, i, vp, vp, vp, vp, i, i, f] + [vp] * 7 + [sz, vp]
+    L.kdn_window_attn.argtypes = [dims, i, vp, vp, vp, vp, i, i, i, f, vp, vp, vp, sz, vp]
+    L.kdn_window_attn_backward.argtypes = [dims, i, vp, vp, vp, vp, i, i, i, f] + [vp] * 7 + [sz, vp]
     L.kdn_window_workspace_bytes.argtypes = [dims, i, i, i, i]
     L.kdn_pages_reserve.argtypes = [pages, i, vp, vp, i, vp, sz, vp]
     L.kdn_pages_fork.argtypes = [pages, i, vp, vp, vp, vp, sz, vp]
@@ -509,9 +509,13 @@ def _on(stream):
     return _SAME if stream is None else torch.cuda.stream(stream)
 
 
+# the current stream's handle without building a Stream object, where torch offers it (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     return stream.cuda_stream
@@ -530,19 +534,20 @@ def _scratch(workspace, need, dev):
 
 
 def _window_args(q, k, v, lens, scale):
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
-        raise ValueError("q must be [B, H, L, d_k], k [B, kv_heads, L, d_k] and v [B, kv_heads, L, d_v]")
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported input dtype {q.dtype}")
-    B, H, L, dk = q.shape
-    Hkv, dv = k.shape[1], v.shape[-1]
-    dev = q.device
-    _need(q, "q", (B, H, L, dk), q.dtype)
-    _need(k, "k", (B, Hkv, L, dk), q.dtype, dev)
-    _need(v, "v", (B, Hkv, L, dv), q.dtype, dev)
+    try:
+        B, H, L, dk = q.shape
+        _, Hkv, _, dv = v.shape
+    except ValueError:
+        raise ValueError("q must be [B, H, L, d_k], k [B, kv_heads, L, d_k] and v [B, kv_heads, L, d_v]") from None
+    dtype, dev = q.dtype, q.device
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported input dtype {dtype}")
+    _need(q, "q", (B, H, L, dk), dtype)
+    _need(k, "k", (B, Hkv, L, dk), dtype, dev)
+    _need(v, "v", (B, Hkv, L, dv), dtype, dev)
     if lens is not None:
         _need(lens, "lens", (B,), torch.int32, dev)
-    return B, H, Hkv, L, dk, dv, dev, float(dk ** -0.5 if scale is None else scale)
+    return B, H, Hkv, L, dk, dv, dev, dk ** -0.5 if scale is None else float(scale)
 
 
 def window_workspace_bytes(B, H, Hkv, L, dk, dv, window, n_sink=0, in_dtype=torch.bfloat16, out_dtype=None, backward=False):
@@ -563,20 +568,26 @@ def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=No
     if out_dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {out_dtype}")
     dims = Dims(B, H, L, dk, dv, 0, _DTYPES[q.dtype], _DTYPES[out_dtype], 0)
-    new = torch.empty if lens is None else torch.zeros
-    with _on(stream):
-        if o is None:
-            o = new(B, H, L, dv, dtype=out_dtype, device=dev)
-        if lse is None:
-            lse = new(B, H, L, dtype=torch.float32, device=dev)
+    if o is not None:
+        _need(o, "o", (B, H, L, dv), out_dtype, dev)
+    if lse is not None:
+        _need(lse, "lse", (B, H, L), torch.float32, dev)
+    fresh = o is None and lse is None
+    if o is None or lse is None:
+        # rows behind the sequences: the kernels zero them where both arrays are new, a fill does where one is
+        new = torch.empty if lens is None or fresh else torch.zeros
+        with _on(stream):
+            if o is None:
+                o = new((B, H, L, dv), dtype=out_dtype, device=dev)
+            if lse is None:
+                lse = new((B, H, L), dtype=torch.float32, device=dev)
     if workspace is not None:
         _scratch(workspace, 256, dev)
-    _need(o, "o", (B, H, L, dv), out_dtype, dev)
-    _need(lse, "lse", (B, H, L), torch.float32, dev)
-    st = lib().kdn_window_attn(ctypes.byref(dims), Hkv, _at(q), _at(k), _at(v), _at(lens), window, n_sink, scale,
-                               _at(o), _at(lse), _at(workspace), 0 if workspace is None else workspace.numel(),
-                               _stream_of(stream, dev))
-    _check(st, "kdn_window_attn")
+    st = lib().kdn_window_attn(dims, Hkv, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(lens), fresh, window, n_sink, scale,
+                               o.data_ptr(), lse.data_ptr(), _at(workspace),
+                               0 if workspace is None else workspace.numel(), _stream_of(stream, dev))
+    if st:
+        _check(st, "kdn_window_attn")
     return o, lse
 
 
@@ -586,25 +597,28 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
     dq, dk, dv in q's type (dk and dv summed over the heads that share them); rows behind a sequence's last token are
     left as they were in given tensors, and are zero in those allocated here."""
     B, H, Hkv, L, d_k, d_v, dev, scale = _window_args(q, k, v, lens, scale)
+    dtype = q.dtype
     if o.dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {o.dtype}")
     _need(o, "o", (B, H, L, d_v), o.dtype, dev)
     _need(lse, "lse", (B, H, L), torch.float32, dev)
     _need(dO, "dO", (B, H, L, d_v), o.dtype, dev)
-    dims = Dims(B, H, L, d_k, d_v, 0, _DTYPES[q.dtype], _DTYPES[o.dtype], 0)
-    new = torch.empty if lens is None else torch.zeros
+    dims = Dims(B, H, L, d_k, d_v, 0, _DTYPES[dtype], _DTYPES[o.dtype], 0)
+    fresh = dq is None and dk is None and dv is None
+    new = torch.empty_like if lens is None or fresh else torch.zeros_like
     with _on(stream):
-        dq = new(B, H, L, d_k, dtype=q.dtype, device=dev) if dq is None else dq
-        dk = new(B, Hkv, L, d_k, dtype=q.dtype, device=dev) if dk is None else dk
-        dv = new(B, Hkv, L, d_v, dtype=q.dtype, device=dev) if dv is None else dv
-        workspace = _scratch(workspace, lib().kdn_window_workspace_bytes(ctypes.byref(dims), Hkv, window, n_sink, 1), dev)
-    _need(dq, "dq", (B, H, L, d_k), q.dtype, dev)
-    _need(dk, "dk", (B, Hkv, L, d_k), q.dtype, dev)
-    _need(dv, "dv", (B, Hkv, L, d_v), q.dtype, dev)
-    st = lib().kdn_window_attn_backward(ctypes.byref(dims), Hkv, _at(q), _at(k), _at(v), _at(lens), window, n_sink,
-                                        scale, _at(o), _at(lse), _at(dO), _at(dq), _at(dk), _at(dv),
-                                        _at(workspace), workspace.numel(), _stream_of(stream, dev))
-    _check(st, "kdn_window_attn_backward")
+        dq = new(q) if dq is None else _need(dq, "dq", (B, H, L, d_k), dtype, dev)
+        dk = new(k) if dk is None else _need(dk, "dk", (B, Hkv, L, d_k), dtype, dev)
+        dv = new(v) if dv is None else _need(dv, "dv", (B, Hkv, L, d_v), dtype, dev)
+        if workspace is None:
+            workspace = _scratch(None, lib().kdn_window_workspace_bytes(dims, Hkv, window, n_sink, 1), dev)
+        else:
+            _scratch(workspace, 256, dev)
+    st = lib().kdn_window_attn_backward(dims, Hkv, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(lens), fresh, window, n_sink,
+                                        scale, o.data_ptr(), lse.data_ptr(), dO.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                        dv.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, dev))
+    if st:
+        _check(st, "kdn_window_attn_backward")
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -623,15 +637,16 @@ class Pages:
     workspace: torch.Tensor | None = None
 
     def _c(self, dev=None):
-        if self.table.dim() != 2:
-            raise ValueError("table must be [rows, max_pages]")
-        rows, most = self.table.shape
-        _need(self.table, "table", (rows, most), torch.int32, dev)
-        dev = self.table.device
-        _need(self.lens, "lens", (rows,), torch.int32, dev)
-        _need(self.refs, "refs", (self.refs.numel(),), torch.int32, dev)
-        return PagesC(self.refs.numel(), self.page_size, rows, most, self.table.data_ptr(), self.lens.data_ptr(),
-                      self.refs.data_ptr())
+        table, lens, refs = self.table, self.lens, self.refs
+        try:
+            rows, most = table.shape
+        except ValueError:
+            raise ValueError("table must be [rows, max_pages]") from None
+        _need(table, "table", (rows, most), torch.int32, dev)
+        dev = table.device
+        _need(lens, "lens", (rows,), torch.int32, dev)
+        _need(refs, "refs", (refs.numel(),), torch.int32, dev)
+        return PagesC(refs.numel(), self.page_size, rows, most, table.data_ptr(), lens.data_ptr(), refs.data_ptr())
 
 
 def make_pages(num_pages, page_size, rows, max_pages, device="cuda") -> Pages:
@@ -643,7 +658,7 @@ def make_pages(num_pages, page_size, rows, max_pages, device="cuda") -> Pages:
 def _list(t, name, dev):
     if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise ValueError(f"{name} must be a 1-D int32 tensor")
-    return _need(t, name, (t.shape[0],), torch.int32, dev)
+    return _need(t, name, t.shape, torch.int32, dev)
 
 
 def _books(pages, stream):
@@ -662,9 +677,10 @@ def pages_reserve(pages, rows, counts, stream=None):
     each = isinstance(counts, torch.Tensor)
     if each:
         _need(counts, "counts", rows.shape, torch.int32, dev)
-    st = lib().kdn_pages_reserve(ctypes.byref(c), rows.numel(), _at(rows), _at(counts) if each else None,
+    st = lib().kdn_pages_reserve(c, rows.numel(), _at(rows), _at(counts) if each else None,
                                  0 if each else counts, _at(ws), ws.numel(), _stream_of(stream, dev))
-    _check(st, "kdn_pages_reserve")
+    if st:
+        _check(st, "kdn_pages_reserve")
 
 
 def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
@@ -677,9 +693,10 @@ def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
         if moves is None:
             moves = torch.empty(src_rows.numel(), 2, dtype=torch.int32, device=dev)
     _need(moves, "moves", (src_rows.numel(), 2), torch.int32, dev)
-    st = lib().kdn_pages_fork(ctypes.byref(c), src_rows.numel(), _at(src_rows), _at(dst_rows), _at(moves), _at(ws),
+    st = lib().kdn_pages_fork(c, src_rows.numel(), _at(src_rows), _at(dst_rows), _at(moves), _at(ws),
                               ws.numel(), _stream_of(stream, dev))
-    _check(st, "kdn_pages_fork")
+    if st:
+        _check(st, "kdn_pages_fork")
     return moves
 
 
@@ -687,8 +704,9 @@ def pages_free(pages, rows, stream=None):
     """Empties the listed rows; pages that no row names any more are free."""
     c, dev, ws = _books(pages, stream)
     _list(rows, "rows", dev)
-    st = lib().kdn_pages_free(ctypes.byref(c), rows.numel(), _at(rows), _at(ws), ws.numel(), _stream_of(stream, dev))
-    _check(st, "kdn_pages_free")
+    st = lib().kdn_pages_free(c, rows.numel(), _at(rows), _at(ws), ws.numel(), _stream_of(stream, dev))
+    if st:
+        _check(st, "kdn_pages_free")
 
 
 def pages_compact(pages, moves=None, stream=None):
@@ -699,18 +717,21 @@ def pages_compact(pages, moves=None, stream=None):
         if moves is None:
             moves = torch.empty(c.num_pages // 2, 2, dtype=torch.int32, device=dev)
     _need(moves, "moves", (c.num_pages // 2, 2), torch.int32, dev)
-    st = lib().kdn_pages_compact(ctypes.byref(c), _at(moves), _at(ws), ws.numel(), _stream_of(stream, dev))
-    _check(st, "kdn_pages_compact")
+    st = lib().kdn_pages_compact(c, _at(moves), _at(ws), ws.numel(), _stream_of(stream, dev))
+    if st:
+        _check(st, "kdn_pages_compact")
     return moves
 
 
 def _pool(k_pages, v_pages, dev=None):
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or v_pages.dim() != 4:
-        raise ValueError("k_pages must be [num_pages, kv_heads, page_size, d_k] and v_pages [num_pages, kv_heads, page_size, d_v]")
+    try:
+        num, Hkv, page, dk = k_pages.shape
+        _, _, _, dv = v_pages.shape
+    except ValueError:
+        raise ValueError("k_pages must be [num_pages, kv_heads, page_size, d_k] and v_pages "
+                         "[num_pages, kv_heads, page_size, d_v]") from None
     if k_pages.dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {k_pages.dtype} of k_pages")
-    num, Hkv, page, dk = k_pages.shape
-    dv = v_pages.shape[-1]
     _need(k_pages, "k_pages", (num, Hkv, page, dk), k_pages.dtype, dev)
     _need(v_pages, "v_pages", (num, Hkv, page, dv), k_pages.dtype, k_pages.device)
     return num, Hkv, page, dk, dv
@@ -723,7 +744,8 @@ def pages_copy(moves, k_pages, v_pages, stream=None):
     _need(moves, "moves", (moves.shape[0], 2), torch.int32, dev)
     st = lib().kdn_pages_copy(moves.shape[0], _at(moves), num, page, Hkv, dk, dv, _DTYPES[k_pages.dtype], _at(k_pages),
                               _at(v_pages), _stream_of(stream, dev))
-    _check(st, "kdn_pages_copy")
+    if st:
+        _check(st, "kdn_pages_copy")
 
 
 def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream=None):
@@ -743,9 +765,10 @@ def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream
     _need(v_new, "v_new", (n, Hkv, T, dv), k_pages.dtype, dev)
     if counts is not None:
         _need(counts, "counts", (n,), torch.int32, dev)
-    st = lib().kdn_pages_write(ctypes.byref(c), n, _at(rows), _at(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype],
+    st = lib().kdn_pages_write(c, n, _at(rows), _at(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype],
                                _at(k_new), _at(v_new), _at(k_pages), _at(v_pages), _stream_of(stream, dev))
-    _check(st, "kdn_pages_write")
+    if st:
+        _check(st, "kdn_pages_write")
 
 
 def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sink=0, scale=None, o=None, lse=None,
@@ -769,20 +792,23 @@ def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sin
     out_dtype = out_dtype or (q.dtype if o is None else o.dtype)
     if out_dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {out_dtype}")
+    if o is not None:
+        _need(o, "o", (n, H, dv), out_dtype, dev)
+    if lse is not None:
+        _need(lse, "lse", (n, H), torch.float32, dev)
     c = PagesC(num, page, table.shape[0], table.shape[1], table.data_ptr(), lens.data_ptr(), None)
     with _on(stream):
         if o is None:
-            o = torch.empty(n, H, dv, dtype=out_dtype, device=dev)
+            o = torch.empty((n, H, dv), dtype=out_dtype, device=dev)
         if lse is None:
-            lse = torch.empty(n, H, dtype=torch.float32, device=dev)
-        need = lib().kdn_paged_step_workspace_bytes(ctypes.byref(c), n, H, Hkv, dk, dv, _DTYPES[q.dtype], window, n_sink)
+            lse = torch.empty((n, H), dtype=torch.float32, device=dev)
+        need = lib().kdn_paged_step_workspace_bytes(c, n, H, Hkv, dk, dv, _DTYPES[q.dtype], window, n_sink)
         if workspace is not None or need > 256:
             workspace = _scratch(workspace, need, dev)
-    _need(o, "o", (n, H, dv), out_dtype, dev)
-    _need(lse, "lse", (n, H), torch.float32, dev)
     scale = float(dk ** -0.5 if scale is None else scale)
-    st = lib().kdn_paged_attn_step(ctypes.byref(c), n, _at(rows), H, Hkv, dk, dv, _DTYPES[q.dtype], _DTYPES[out_dtype],
+    st = lib().kdn_paged_attn_step(c, n, _at(rows), H, Hkv, dk, dv, _DTYPES[q.dtype], _DTYPES[out_dtype],
                                    _at(q), _at(k_pages), _at(v_pages), window, n_sink, scale, _at(o), _at(lse),
                                    _at(workspace), 0 if workspace is None else workspace.numel(), _stream_of(stream, dev))
-    _check(st, "kdn_paged_attn_step")
+    if st:
+        _check(st, "kdn_paged_attn_step")
     return o, lse

@@ -291,14 +291,14 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * q [B,H,L,d_k], k [B,kv_heads,L,d_k], v [B,kv_heads,L,d_v] (dims->in_dtype): query head h reads k/v head
  * h / (H / kv_heads); kv_heads divides H.  lens [B] int32 or NULL (= L): tokens of each sequence, held to
  * [0, L]; what memory holds behind a sequence's last token takes no part (it may be NaN), and its rows of o
- * and lse are left as they were.  window >= 1 (>= L: plain causal attention), n_sink >= 0, scale > 0.
+ * and lse are left as they were (zero_rest = 0) or set to zero (1).  window >= 1 (>= L: plain causal attention), n_sink >= 0, scale > 0.
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
  * enter the second product as bf16; sums, maxima and both products' accumulators are fp32), everything else
  * on the fp32 cores.  workspace: 256 bytes for the status word, or NULL: none is kept (a bounded wait that gives
  * up also leaves NaN in its rows of lse).  Asynchronous. */
 KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
-                           const int* lens, int window, int n_sink, float scale, void* o, float* lse,
+                           const int* lens, int zero_rest, int window, int n_sink, float scale, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* Backward of kdn_window_attn: from the forward's inputs, its o and lse and the upstream dO [B,H,L,d_v]
@@ -307,10 +307,10 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  * delta_t = dO_t . o_t, P_tj = exp(scale q_t . k_j - lse_t) and dS_tj = P_tj (dO_t . v_j - delta_t):
  *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
  * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
- * gradients do not change from run to run.  Rows behind a sequence's last token are left as they were; lse has
- * no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1) bytes. */
+ * gradients do not change from run to run.  Rows behind a sequence's last token are left as they were or set to
+ * zero (zero_rest), in all three; lse has no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
-                                    const void* v, const int* lens, int window, int n_sink, float scale,
+                                    const void* v, const int* lens, int zero_rest, int window, int n_sink, float scale,
                                     const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
                                     void* workspace, size_t workspace_bytes, void* stream);
 

@@ -64,7 +64,7 @@ def L():
 
 
 def _attn(L, d, kv=1, window=4, n_sink=0, scale=1.0):
-    return L.kdn_window_attn(ctypes.byref(d), kv, None, None, None, None, window, n_sink, scale, None, None, None, 0, None)
+    return L.kdn_window_attn(ctypes.byref(d), kv, None, None, None, None, 0, window, n_sink, scale, None, None, None, 0, None)
 
 
 def test_window_attention_refusals(L):
@@ -78,7 +78,7 @@ def test_window_attention_refusals(L):
     assert _attn(L, kdn.Dims(1, 4, 8, 48, 64, 0, 1, 1, 0)) == kdn.KDN_ERR_UNSUPPORTED
     assert _attn(L, kdn.Dims(1 << 14, 1 << 10, 1 << 14, 64, 64, 0, 1, 1, 0)) == kdn.KDN_ERR_UNSUPPORTED
     assert _attn(L, d) == kdn.KDN_ERR_INVALID_ARG and b"q is NULL" in L.kdn_last_error()
-    args = [None] * 3 + [None, 4, 0, 1.0] + [None] * 7 + [0, None]
+    args = [None] * 3 + [None, 0, 4, 0, 1.0] + [None] * 7 + [0, None]
     assert L.kdn_window_attn_backward(ctypes.byref(d), 1, *args) == kdn.KDN_ERR_INVALID_ARG
     assert L.kdn_window_workspace_bytes(ctypes.byref(d), 3, 4, 0, 1) == 0
     assert L.kdn_window_workspace_bytes(ctypes.byref(d), 2, 4, 0, 0) >= 256

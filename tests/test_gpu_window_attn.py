@@ -130,6 +130,11 @@ def test_padded_batch_with_nan_behind_the_sequences(dtype, d, window, n_sink):
     o, lse, g = _check(q, k, v, dO, window, n_sink, lens)
     o0, lse0, g0 = _check(*clean, window, n_sink, lens)
     assert torch.equal(o, o0) and torch.equal(lse, lse0) and all(torch.equal(g[x], g0[x]) for x in g)
+    for x in (o, lse, *g.values()):  # rows of arrays that the call made itself are zero
+        for b, n in enumerate(lens.clamp(0, L).tolist()):
+            assert bool((x[b, :, n:] == 0).all())
+    half, _ = kdn.window_attn(q, k, v, window, n_sink=n_sink, lens=lens, lse=torch.full_like(lse, 7.0))
+    assert torch.equal(half, o)
     o = torch.full_like(o, 7.0)
     lse = torch.full_like(lse, 7.0)
     kdn.window_attn(q, k, v, window, n_sink=n_sink, lens=lens, o=o, lse=lse)
