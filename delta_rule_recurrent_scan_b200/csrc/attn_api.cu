@@ -116,7 +116,7 @@ size_t kdn_window_workspace_bytes(const kdn_dims* dims, int kv_heads, int window
   if (kdn::window_tc_supported(dims->dk, dims->dv, dims->in_dtype))
     n += round256(kdn::window_bwd_tc_scratch_bytes(dims->B, dims->H, kv_heads, dims->L, dims->dk, dims->out_dtype, window, n_sink));
   else
-    n += round256((size_t)dims->B * dims->H * (size_t)dims->L * sizeof(float));
+    n += round256(kdn::window_bwd_scratch_bytes(dims->B, dims->H, kv_heads, dims->L, dims->dk, dims->dv, window, n_sink));
   return n;
 }
 

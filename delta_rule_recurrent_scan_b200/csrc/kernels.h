@@ -275,13 +275,14 @@ struct WindowArgs {
   void* dq;             // in_dtype
   void* dk;
   void* dv;
-  void* scratch;        // tensor-core path: window_bwd_tc_scratch_bytes
+  void* scratch;        // backward: window_bwd_scratch_bytes or window_bwd_tc_scratch_bytes
 };
 cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& args, cudaStream_t stream);
 // tensor-core variant (bf16, d_k = d_v = 64 or 128); launch_window_attn picks it when it applies
 bool window_tc_supported(int dk, int dv, int in_dtype);
 cudaError_t launch_window_attn_tc(int d, const WindowArgs& args, cudaStream_t stream);
 cudaError_t launch_window_bwd_tc(int d, const WindowArgs& args, cudaStream_t stream);
+size_t window_bwd_scratch_bytes(int B, int H, int Hkv, int L, int dk, int dv, int window, int n_sink);
 size_t window_bwd_tc_scratch_bytes(int B, int H, int Hkv, int L, int d, int out_dtype, int window, int n_sink);
 cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& args, cudaStream_t stream);
 

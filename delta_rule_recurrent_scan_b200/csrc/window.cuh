@@ -71,5 +71,45 @@ __host__ __device__ __forceinline__ void query_tiles(int j0, int j1, int len, in
   hi = t1 / T + 1;
 }
 
+// The keys' pass of the backward.  The key tiles that hold sinks are seen by every later query; where there are one or two
+// of them their walk is cut into parts of a regular tile's length, whose fp32 sums go to ``part`` and are added in order
+// by a launch of their own.
+struct KeyPass {
+  int sinks, parts;  // key tiles that are cut, and into how many parts (0, 1: none)
+  float* part;
+  int tile, head;    // of this CTA (key_tile_of)
+};
+// Tiles of K keys walk tiles of Q queries.
+template <int K, int Q>
+inline KeyPass key_pass(int H, int Hkv, int L, int window, int n_sink) {
+  const int tiles = (L + K - 1) / K, walk = (L + Q - 1) / Q;
+  const int sinks = n_sink <= 0 ? 0 : n_sink < L ? (n_sink - 1) / K + 1 : tiles;
+  KeyPass kp{0, 1, nullptr, 0, 0};
+  if (sinks == 0 || sinks > 2 || sinks >= tiles) return kp;
+  const int regular = (window + K - 2) / Q + 2;    // query tiles that see a tile within the window
+  const long long items = (long long)walk * (H / Hkv);
+  long long parts = (walk + regular - 1) / regular;
+  if (parts > 64) parts = 64;
+  if (parts > items / 4) parts = items / 4;        // a part shorter than four tiles is all start-up
+  if (parts < 2) return kp;
+  kp.sinks = sinks, kp.parts = static_cast<int>(parts);
+  return kp;
+}
+// Key tile and (sequence, k/v head) of CTA x: the cut walks come first (they are the longest), then the other key tiles.
+// True for a cut tile, whose part it is then.
+__device__ __forceinline__ bool key_tile_of(KeyPass& kp, int heads, int tiles, unsigned x, int& part) {
+  const unsigned cut = (unsigned)heads * kp.sinks * kp.parts;
+  part = 0;
+  if (x < cut) {
+    part = x % kp.parts, x /= kp.parts;
+    kp.tile = x % kp.sinks, kp.head = x / kp.sinks;
+    return true;
+  }
+  x -= cut;
+  const int rest = tiles - kp.sinks;
+  kp.tile = kp.sinks + x % rest, kp.head = x / rest;
+  return false;
+}
+
 }  // namespace window
 }  // namespace kdn

@@ -1,14 +1,24 @@
 // Windowed attention on the fp32 CUDA cores: every supported size and type.
 //
 //   vis(t) = { j <= t : j > t - window or j < n_sink },  s_tj = scale q_t . k_j,
-//   lse_t = log sum_vis exp s_tj,  o_t = sum_vis exp(s_tj - lse_t) v_j.
+//   lse_t = log sum_vis exp s_tj,  o_t = sum_vis exp(s_tj - lse_t) v_j,
+//   dv = P^T dO,  dq = scale dS k,  dk = scale dS^T q,  dS = P (dO v^T - delta),  delta_t = dO_t . o_t.
 //
-// One CTA of 256 threads per 64 queries of a head walks the 64-token key tiles that any of them sees (the sinks'
-// tiles, then the window's), with the running maximum and sum of the softmax in registers.  A thread holds 4 x 4
-// scores (queries ty + 16 i, keys tx + 16 j) and the same 4 queries of o.  Rows are padded by 4 floats in shared
-// memory, so that the 16-byte reads of 8 consecutive rows fall into 8 different bank groups.  Per 4 coordinates a
-// warp spends 64 multiply-adds against 12 shared-memory wavefronts (16 issue cycles of the SM's four schedulers
-// against 12): bound by the fp32 pipe.  Rows past the sequence's end are staged as zeros, whatever memory holds.
+// All three kernels are one scheme.  A CTA of 8 warps owns 8 R rows (queries; keys for dk and dv) and walks the 64-row
+// tiles of the other side that they meet, staged in shared memory as fp32.  A warp has R rows, the same for all of its
+// lanes, and a lane has 2 of the 64 columns:
+//   scores:   s[R][2] += row . column; a row's 16 bytes are one broadcast read for the whole warp, the columns' rows are
+//             padded by 4 floats so that 8 consecutive lanes fall into 8 different bank groups.  Per 4 coordinates a warp
+//             spends 8 R multiply-adds against R + 8 wavefronts;
+//   weights:  exp, masks, row maxima and sums within the warp; the R x 64 weights go to a piece of shared memory of the
+//             warp's own (no CTA barrier between scores and products);
+//   products: acc[R][d / 32] += weight x tile row, again with the weights as broadcast reads.
+// R is 8, or 4 where 8 would leave SMs without a CTA.  Measured (fp32, 3 padded sequences of 1531, 8 heads of 64, window
+// 257, 16 sinks): forward 117 us, backward 384 us; the fp32 pipe is 37 % busy where a CTA runs, the rest waits for
+// shared-memory reads.  4 x 4 values per thread with the rows spread over the lanes (four wavefronts a read): 121 and
+// 615 us; R = 16 (one CTA per SM, longer tail): 163 and 404 us; three CTAs per SM (spills): 146 and 464 us.
+//
+// Rows past the sequence's end are staged as zeros, whatever memory holds.
 #include <cmath>
 #include <type_traits>
 
@@ -18,17 +28,20 @@ namespace kdn {
 
 namespace {
 
+using window::KeyPass;
 using window::KeyTiles;
 
-constexpr int kThreads = 256;
-constexpr int kT = 64;       // queries and keys per tile
-constexpr int kLP = kT + 4;  // row stride of the score tile
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kT = 64;       // rows of a walked tile
+constexpr int kLP = kT + 4;  // row stride of the weights
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Rows t0 .. t0 + 63 of a [L, D] array into shared memory as fp32; rows at or past ``len`` become zero.
-template <int D>
+// Rows t0 .. t0 + ROWS - 1 of a [L, D] array into shared memory as fp32; rows at or past ``len`` become zero.
+template <int D, int ROWS>
 __device__ __forceinline__ void stage(float* dst, const void* src, size_t row0, int t0, int len, int dtype) {
   constexpr int Q = D / 4;
-  for (int e = threadIdx.x; e < kT * Q; e += kThreads) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < ROWS * Q; e += kThreads) {
     const int r = e / Q, c = 4 * (e % Q);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t0 + r < len) {
@@ -45,109 +58,107 @@ __device__ __forceinline__ void stage(float* dst, const void* src, size_t row0, 
   }
 }
 
-// acc[i][j] += a[ra + 16 i] . b[rb + 16 j] over D coordinates.
-template <int D>
-__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float* a, int ra, const float* b, int rb) {
+// s[i][c] = rows[i] . tile[lane + 32 c]
+template <int D, int R>
+__device__ __forceinline__ void scores(float (&s)[R][2], const float* rows, const float* tile, int lane) {
   constexpr int S = D + 4;
-  float2 sum[4][4] = {};  // even and odd coordinates
-#pragma unroll 4
-  for (int c = 0; c < D; c += 4) {
-    float4 x[4], y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ra + 16 * i) * S + c);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (rb + 16 * j) * S + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sum[i][j] = window::fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w),
-                                 window::fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]));
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] += sum[i][j].x + sum[i][j].y;
-}
-
-// a[n] += w b[n], two at a time.
-template <int N>
-__device__ __forceinline__ void axpy(float (&a)[N], float w, const float (&b)[N]) {
-  if constexpr (N % 2 == 0) {
-#pragma unroll
-    for (int n = 0; n < N; n += 2) {
-      const float2 r = window::fma2(make_float2(w, w), make_float2(b[n], b[n + 1]), make_float2(a[n], a[n + 1]));
-      a[n] = r.x, a[n + 1] = r.y;
-    }
-  } else {
-#pragma unroll
-    for (int n = 0; n < N; ++n) a[n] = fmaf(w, b[n], a[n]);
-  }
-}
-
-// Column (of D) that value n (of D / 16) of thread column tx stands for: float4 groups where the row is wide enough.
-template <int D>
-__device__ __forceinline__ int col_of(int tx, int n) {
-  return D >= 64 ? 64 * (n / 4) + 4 * tx + n % 4 : tx + 16 * n;
-}
-// One row's D / 16 values of a thread.
-template <int D>
-__device__ __forceinline__ void row_vals(float (&x)[D / 16], const float* row, int tx) {
-  if constexpr (D >= 64) {
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g) {
-      const float4 u = *reinterpret_cast<const float4*>(row + 64 * g + 4 * tx);
-      x[4 * g] = u.x, x[4 * g + 1] = u.y, x[4 * g + 2] = u.z, x[4 * g + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) x[n] = row[tx + 16 * n];
-  }
-}
-
-// acc[i][n] += sum_j w[(r + 16 i)][j] b[j][col n]: the row-times-tile product (o += P v, dq += dS k).
-template <int D>
-__device__ __forceinline__ void rows_times_tile(float (&acc)[4][D / 16], const float* w, int r, const float* b, int tx) {
+  float2 sum[R][2] = {};  // even and odd coordinates
 #pragma unroll 2
-  for (int j = 0; j < kT; j += 4) {
-    float4 p[4];
+  for (int c = 0; c < D; c += 4) {
+    const float4 y0 = *reinterpret_cast<const float4*>(tile + lane * S + c);
+    const float4 y1 = *reinterpret_cast<const float4*>(tile + (lane + 32) * S + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(w + (r + 16 * i) * kLP + j);
+    for (int i = 0; i < R; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(rows + i * S + c);
+      const float2 a = make_float2(x.x, x.y), b = make_float2(x.z, x.w);
+      sum[i][0] = window::fma2(b, make_float2(y0.z, y0.w), window::fma2(a, make_float2(y0.x, y0.y), sum[i][0]));
+      sum[i][1] = window::fma2(b, make_float2(y1.z, y1.w), window::fma2(a, make_float2(y1.x, y1.y), sum[i][1]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) s[i][0] = sum[i][0].x + sum[i][0].y, s[i][1] = sum[i][1].x + sum[i][1].y;
+}
+
+// Values of a row that a lane holds: d / 32 consecutive ones; with d = 16 one, the half-warps sharing the tile's rows.
+template <int D>
+constexpr int kVals = D < 32 ? 1 : D / 32;
+template <int D>
+__device__ __forceinline__ int first_col(int lane) {
+  return D < 32 ? lane % D : lane * kVals<D>;
+}
+
+// acc[i] += sum_j w[i][j] tile[j]: the products with the weights of this warp.
+template <int D, int R>
+__device__ __forceinline__ void products(float (&acc)[R][kVals<D>], const float* w, const float* tile, int lane) {
+  constexpr int S = D + 4, V = kVals<D>;
+  const float* at = tile + first_col<D>(lane);
+  const int j0 = D < 32 ? (lane / D) * (kT / 2) : 0, j1 = D < 32 ? j0 + kT / 2 : kT;
+#pragma unroll 2
+  for (int j = j0; j < j1; j += 4) {
+    float x[4][V];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      float x[D / 16];
-      row_vals<D>(x, b + (j + u) * (D + 4), tx);
+      const float* row = at + (j + u) * S;
+      if constexpr (V == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(row);
+        x[u][0] = y.x, x[u][1] = y.y, x[u][2] = y.z, x[u][3] = y.w;
+      } else if constexpr (V == 2) {
+        const float2 y = *reinterpret_cast<const float2*>(row);
+        x[u][0] = y.x, x[u][1] = y.y;
+      } else {
+        x[u][0] = *row;
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        axpy(acc[i], u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w, x);
+    for (int i = 0; i < R; ++i) {
+      const float4 p = *reinterpret_cast<const float4*>(w + i * kLP + j);
+      const float pw[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if constexpr (V == 1) {
+          acc[i][0] = fmaf(pw[u], x[u][0], acc[i][0]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < V; n += 2) {
+            const float2 r = window::fma2(make_float2(pw[u], pw[u]), make_float2(x[u][n], x[u][n + 1]),
+                                          make_float2(acc[i][n], acc[i][n + 1]));
+            acc[i][n] = r.x, acc[i][n + 1] = r.y;
+          }
+        }
       }
     }
   }
 }
 
-// acc[i][n] += sum_t w[t][4 ty + i] b[t][col n]: the transposed product (dv += P^T dO, dk += dS^T q).
+// Write a lane's values of one row, times f.
 template <int D>
-__device__ __forceinline__ void cols_times_tile(float (&acc)[4][D / 16], const float* w, int ty, const float* b, int tx) {
-#pragma unroll 4
-  for (int t = 0; t < kT; ++t) {
-    const float4 p = *reinterpret_cast<const float4*>(w + t * kLP + 4 * ty);
-    float x[D / 16];
-    row_vals<D>(x, b + t * (D + 4), tx);
-    axpy(acc[0], p.x, x), axpy(acc[1], p.y, x), axpy(acc[2], p.z, x), axpy(acc[3], p.w, x);
+__device__ __forceinline__ void put_row(void* dst, size_t row, const float (&x)[kVals<D>], float f, int lane, int dtype) {
+  if constexpr (D < 32) {
+    const float y = x[0] + __shfl_xor_sync(0xffffffffu, x[0], D);  // the other half-warp's part
+    if (lane < D) store_elem(dst, row * D + lane, y * f, dtype);
+  } else {
+    const size_t at = row * D + first_col<D>(lane);
+#pragma unroll
+    for (int n = 0; n < kVals<D>; ++n) store_elem(dst, at + n, x[n] * f, dtype);
   }
 }
 
-// Write a thread's values of one row.
-template <int D>
-__device__ __forceinline__ void put_row(void* dst, size_t row, const float (&x)[D / 16], float f, int tx, int dtype) {
+// For R values of every lane: the warp's maximum (KIND 0) or sum (1) of each, in all lanes.
+template <int KIND, int R>
+__device__ __forceinline__ void reduce_rows(float (&x)[R]) {
 #pragma unroll
-  for (int n = 0; n < D / 16; ++n) store_elem(dst, row * D + col_of<D>(tx, n), x[n] * f, dtype);
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x[i], o);
+      x[i] = KIND == 0 ? fmaxf(x[i], y) : x[i] + y;
+    }
 }
 
-// Rows t .. t0 + 63 (t = the sequence's end, or t0 where the tile lies behind it) of a [L, D] array become zero.
-template <int D>
+// Rows max(t0, len) .. t0 + ROWS - 1 of a [L, D] array become zero.
+template <int D, int ROWS>
 __device__ __forceinline__ void zero_tile(void* dst, size_t row0, int t0, int len, int L, int dtype) {
-  const int first = max(t0, len), last = min(t0 + kT, L), words = D * (dtype == kBF16 ? 2 : 4) / 16;
+  const int first = max(t0, len), last = min(t0 + ROWS, L), words = D * (dtype == kBF16 ? 2 : 4) / 16;
   for (int e = threadIdx.x; e < (last - first) * words; e += kThreads)
     static_cast<uint4*>(dst)[(row0 + first) * words + e] = make_uint4(0, 0, 0, 0);
 }
@@ -156,8 +167,7 @@ __device__ __forceinline__ void zero_tile(void* dst, size_t row0, int t0, int le
 struct Where {
   int tile, h, b;
 };
-__device__ __forceinline__ Where where(int tiles, int heads) {
-  const unsigned x = blockIdx.x;
+__device__ __forceinline__ Where where(unsigned x, int tiles, int heads) {
   Where w;
   w.tile = tiles - 1 - static_cast<int>(x % tiles);
   const unsigned y = x / tiles;
@@ -165,77 +175,72 @@ __device__ __forceinline__ Where where(int tiles, int heads) {
   return w;
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int R>
 __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WindowArgs p) {
+  constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
   float* q_s = sm;
-  float* k_s = q_s + kT * (DK + 4);
+  float* k_s = q_s + kRows * (DK + 4);
   float* v_s = k_s + kT * (DK + 4);
   float* p_s = v_s + kT * (DV + 4);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const Where w = where((p.L + kT - 1) / kT, p.H);
-  const int len = window::seq_len(p, w.b), t0 = w.tile * kT;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Where w = where(blockIdx.x, (p.L + kRows - 1) / kRows, p.H);
+  const int len = window::seq_len(p, w.b), t0 = w.tile * kRows;
   const size_t qrow = ((size_t)w.b * p.H + w.h) * p.L;
-  if (p.zero_rest && t0 + kT > len) {
-    zero_tile<DV>(p.o, qrow, t0, len, p.L, p.out_dtype);
+  if (p.zero_rest && t0 + kRows > len) {
+    zero_tile<DV, kRows>(p.o, qrow, t0, len, p.L, p.out_dtype);
     const int t = max(t0, len) + tid;
-    if (t < min(t0 + kT, p.L)) p.lse[qrow + t] = 0.f;
+    if (t < min(t0 + kRows, p.L)) p.lse[qrow + t] = 0.f;
   }
   if (t0 >= len) return;
   const size_t krow = ((size_t)w.b * p.Hkv + w.h / (p.H / p.Hkv)) * p.L;
-  const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kT, len) - 1, p.window, p.n_sink);
-  stage<DK>(q_s, p.q, qrow, t0, len, p.in_dtype);
-  float m[4], l[4], acc[4][DV / 16];
+  const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kRows, len) - 1, p.window, p.n_sink);
+  stage<DK, kRows>(q_s, p.q, qrow, t0, len, p.in_dtype);
+  const float c = p.scale * kLog2e;
+  const int t_w = t0 + warp * R;  // the warp's first query
+  float* w_s = p_s + warp * R * kLP;
+  float m[R], l[R], acc[R][kVals<DV>] = {};  // m in base 2; l: this lane's part of the sum
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m[i] = -INFINITY, l[i] = 0.f;
-#pragma unroll
-    for (int n = 0; n < DV / 16; ++n) acc[i][n] = 0.f;
-  }
+  for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.f;
   for (int it = 0; it < kt.count(); ++it) {
     const int j0 = kt.walk(it) * kT;
     __syncthreads();  // the previous tile has been read
-    stage<DK>(k_s, p.k, krow, j0, len, p.in_dtype);
-    stage<DV>(v_s, p.v, krow, j0, len, p.in_dtype);
+    stage<DK, kT>(k_s, p.k, krow, j0, len, p.in_dtype);
+    stage<DV, kT>(v_s, p.v, krow, j0, len, p.in_dtype);
     __syncthreads();
-    float s[4][4] = {};
-    dot_tile<DK>(s, q_s, ty, k_s, tx);
+    float s[R][2], top[R];
+    scores<DK, R>(s, q_s + warp * R * (DK + 4), k_s, lane);
+    const bool all = j0 + kT - 1 <= t_w && (t_w + R - 1 - j0 < p.window || j0 + kT <= p.n_sink);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + ty + 16 * i;
-      float top = m[i];
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = window::visible(t, j0 + tx + 16 * j, p.window, p.n_sink) ? s[i][j] * p.scale : -INFINITY;
-        top = fmaxf(top, s[i][j]);
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float base = top == -INFINITY ? 0.f : top;  // no key of this row so far
-      const float keep = expf(m[i] - base);
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float e = expf(s[i][j] - base);
-        sum += e;
-        p_s[(ty + 16 * i) * kLP + tx + 16 * j] = e;
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      l[i] = l[i] * keep + sum;
-      m[i] = top;
-#pragma unroll
-      for (int n = 0; n < DV / 16; ++n) acc[i][n] *= keep;
+      for (int n = 0; n < 2; ++n)
+        s[i][n] = all || window::visible(t_w + i, j0 + lane + 32 * n, p.window, p.n_sink) ? s[i][n] * c : -INFINITY;
+      top[i] = fmaxf(s[i][0], s[i][1]);
     }
-    __syncwarp();  // a query row's scores are written and read by the same half-warp
-    rows_times_tile<DV>(acc, p_s, ty, v_s, tx);
-  }
+    reduce_rows<0>(top);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + ty + 16 * i;
-    if (t >= len) continue;
-    put_row<DV>(p.o, qrow + t, acc[i], 1.f / l[i], tx, p.out_dtype);
-    if (tx == 0) p.lse[qrow + t] = m[i] + logf(l[i]);
+    for (int i = 0; i < R; ++i) {
+      top[i] = fmaxf(top[i], m[i]);
+      const float base = top[i] == -INFINITY ? 0.f : top[i];  // no key of this row so far
+      const float keep = exp2f(m[i] - base);
+      const float a = exp2f(s[i][0] - base), b = exp2f(s[i][1] - base);
+      w_s[i * kLP + lane] = a, w_s[i * kLP + lane + 32] = b;
+      l[i] = fmaf(l[i], keep, a + b);
+      m[i] = top[i];
+#pragma unroll
+      for (int n = 0; n < kVals<DV>; ++n) acc[i][n] *= keep;
+    }
+    __syncwarp();
+    products<DV, R>(acc, w_s, v_s, lane);
+  }
+  reduce_rows<1>(l);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int t = t_w + i;
+    if (t >= len) break;
+    put_row<DV>(p.o, qrow + t, acc[i], 1.f / l[i], lane, p.out_dtype);
+    if (lane == 0) p.lse[qrow + t] = (m[i] + log2f(l[i])) * kLn2;
   }
 }
 
@@ -254,165 +259,227 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs p, int dv)
   if (lane == 0) p.delta[row] = x;
 }
 
-// P and dS of one 64 x 64 tile: P = exp(scale q.k - lse), dS = P (dO.v - delta), zero where hidden or past the end.
-template <int DK, int DV>
-__device__ __forceinline__ void grad_scores(const WindowArgs& p, const float* q_s, const float* k_s, const float* do_s,
-                                            const float* v_s, const float* lse_s, const float* delta_s, int t0, int j0,
-                                            int len, int tx, int ty, float (&P)[4][4], float (&dS)[4][4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) P[i][j] = 0.f, dS[i][j] = 0.f;
-  dot_tile<DK>(P, q_s, ty, k_s, tx);
-  dot_tile<DV>(dS, do_s, ty, v_s, tx);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i, t = t0 + r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool vis = t < len && window::visible(t, j0 + tx + 16 * j, p.window, p.n_sink);
-      P[i][j] = vis ? expf(fmaf(P[i][j], p.scale, -lse_s[r])) : 0.f;
-      dS[i][j] = vis ? P[i][j] * (dS[i][j] - delta_s[r]) : 0.f;
-    }
-  }
-}
-
-__device__ __forceinline__ void stage_rows(const WindowArgs& p, float* lse_s, float* delta_s, size_t qrow, int t0, int len) {
-  const int r = threadIdx.x;
-  if (r < kT) {
-    const bool in = t0 + r < len;
-    lse_s[r] = in ? p.lse[qrow + t0 + r] : 0.f;
-    delta_s[r] = in ? p.delta[qrow + t0 + r] : 0.f;
-  }
-}
-
-template <int DK, int DV>
+template <int DK, int DV, int R>
 __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
+  constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
   float* q_s = sm;
-  float* do_s = q_s + kT * (DK + 4);
-  float* k_s = do_s + kT * (DV + 4);
+  float* do_s = q_s + kRows * (DK + 4);
+  float* k_s = do_s + kRows * (DV + 4);
   float* v_s = k_s + kT * (DK + 4);
   float* ds_s = v_s + kT * (DV + 4);
-  float* lse_s = ds_s + kT * kLP;
-  float* delta_s = lse_s + kT;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const Where w = where((p.L + kT - 1) / kT, p.H);
-  const int len = window::seq_len(p, w.b), t0 = w.tile * kT;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Where w = where(blockIdx.x, (p.L + kRows - 1) / kRows, p.H);
+  const int len = window::seq_len(p, w.b), t0 = w.tile * kRows;
   const size_t qrow = ((size_t)w.b * p.H + w.h) * p.L;
-  if (p.zero_rest && t0 + kT > len) zero_tile<DK>(p.dq, qrow, t0, len, p.L, p.in_dtype);
+  if (p.zero_rest && t0 + kRows > len) zero_tile<DK, kRows>(p.dq, qrow, t0, len, p.L, p.in_dtype);
   if (t0 >= len) return;
   const size_t krow = ((size_t)w.b * p.Hkv + w.h / (p.H / p.Hkv)) * p.L;
-  const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kT, len) - 1, p.window, p.n_sink);
-  stage<DK>(q_s, p.q, qrow, t0, len, p.in_dtype);
-  stage<DV>(do_s, p.dO, qrow, t0, len, p.out_dtype);
-  stage_rows(p, lse_s, delta_s, qrow, t0, len);
-  float acc[4][DK / 16] = {};
+  const KeyTiles kt = window::key_tiles<kT>(t0, min(t0 + kRows, len) - 1, p.window, p.n_sink);
+  stage<DK, kRows>(q_s, p.q, qrow, t0, len, p.in_dtype);
+  stage<DV, kRows>(do_s, p.dO, qrow, t0, len, p.out_dtype);
+  const float c = p.scale * kLog2e;
+  const int t_w = t0 + warp * R;
+  float* w_s = ds_s + warp * R * kLP;
+  float lse[R], delta[R], acc[R][kVals<DK>] = {};
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const bool in = t_w + i < len;
+    lse[i] = in ? p.lse[qrow + t_w + i] * kLog2e : 0.f;
+    delta[i] = in ? p.delta[qrow + t_w + i] : 0.f;
+  }
   for (int it = 0; it < kt.count(); ++it) {
     const int j0 = kt.walk(it) * kT;
     __syncthreads();
-    stage<DK>(k_s, p.k, krow, j0, len, p.in_dtype);
-    stage<DV>(v_s, p.v, krow, j0, len, p.in_dtype);
+    stage<DK, kT>(k_s, p.k, krow, j0, len, p.in_dtype);
+    stage<DV, kT>(v_s, p.v, krow, j0, len, p.in_dtype);
     __syncthreads();
-    float P[4][4], dS[4][4];
-    grad_scores<DK, DV>(p, q_s, k_s, do_s, v_s, lse_s, delta_s, t0, j0, len, tx, ty, P, dS);
+    float s[R][2], dp[R][2];
+    scores<DK, R>(s, q_s + warp * R * (DK + 4), k_s, lane);
+    scores<DV, R>(dp, do_s + warp * R * (DV + 4), v_s, lane);
+    const bool all = j0 + kT - 1 <= t_w && (t_w + R - 1 - j0 < p.window || j0 + kT <= p.n_sink);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ds_s[(ty + 16 * i) * kLP + tx + 16 * j] = dS[i][j];
+      for (int n = 0; n < 2; ++n) {
+        const float P = exp2f(fmaf(s[i][n], c, -lse[i]));
+        w_s[i * kLP + lane + 32 * n] =
+            all || window::visible(t_w + i, j0 + lane + 32 * n, p.window, p.n_sink) ? P * (dp[i][n] - delta[i]) : 0.f;
+      }
     __syncwarp();
-    rows_times_tile<DK>(acc, ds_s, ty, k_s, tx);
+    products<DK, R>(acc, w_s, k_s, lane);
+    __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + ty + 16 * i;
-    if (t < len) put_row<DK>(p.dq, qrow + t, acc[i], p.scale, tx, p.in_dtype);
+  for (int i = 0; i < R; ++i) {
+    if (t_w + i >= len) break;
+    put_row<DK>(p.dq, qrow + t_w + i, acc[i], p.scale, lane, p.in_dtype);
   }
 }
 
-// One CTA per 64 keys of a k/v head: it walks every query tile that sees them, of every head that shares them, in a
-// fixed order, so the sums of a gradient are the same on every run.
-template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads) window_dkdv_kernel(WindowArgs p) {
+// The keys' pass: every query tile that sees the CTA's keys, of every head that shares them, in a fixed order, so the sums
+// of a gradient are the same on every run.  Key tiles with sinks may be cut (window::key_pass).
+template <int DK, int DV, int R>
+__global__ void __launch_bounds__(kThreads) window_dkdv_kernel(WindowArgs p, KeyPass kp) {
+  constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
   float* k_s = sm;
-  float* v_s = k_s + kT * (DK + 4);
-  float* q_s = v_s + kT * (DV + 4);
+  float* v_s = k_s + kRows * (DK + 4);
+  float* q_s = v_s + kRows * (DV + 4);
   float* do_s = q_s + kT * (DK + 4);
   float* p_s = do_s + kT * (DV + 4);
-  float* ds_s = p_s + kT * kLP;
-  float* lse_s = ds_s + kT * kLP;
-  float* delta_s = lse_s + kT;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  Where w = where((p.L + kT - 1) / kT, p.Hkv);
-  w.tile = (p.L + kT - 1) / kT - 1 - w.tile;  // the first tiles (sinks) have the longest walk
-  const int len = window::seq_len(p, w.b), j0 = w.tile * kT;
+  float* ds_s = p_s + kRows * kLP;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int part;
+  const bool is_cut = window::key_tile_of(kp, p.B * p.Hkv, (p.L + kRows - 1) / kRows, blockIdx.x, part);
+  const int tile = kp.tile, h = kp.head % p.Hkv, b = kp.head / p.Hkv;
+  const int len = window::seq_len(p, b), j0 = tile * kRows;
   const int G = p.H / p.Hkv;
-  const size_t krow = ((size_t)w.b * p.Hkv + w.h) * p.L;
-  if (p.zero_rest && j0 + kT > len) {
-    zero_tile<DK>(p.dk, krow, j0, len, p.L, p.in_dtype);
-    zero_tile<DV>(p.dv, krow, j0, len, p.L, p.in_dtype);
+  const size_t krow = (size_t)kp.head * p.L;
+  if (p.zero_rest && part == 0 && j0 + kRows > len) {
+    zero_tile<DK, kRows>(p.dk, krow, j0, len, p.L, p.in_dtype);
+    zero_tile<DV, kRows>(p.dv, krow, j0, len, p.L, p.in_dtype);
   }
   if (j0 >= len) return;
   int lo, hi;
-  window::query_tiles<kT>(j0, min(j0 + kT, len) - 1, len, p.window, p.n_sink, lo, hi);
-  stage<DK>(k_s, p.k, krow, j0, len, p.in_dtype);
-  stage<DV>(v_s, p.v, krow, j0, len, p.in_dtype);
-  float dk[4][DK / 16] = {}, dv[4][DV / 16] = {};
-  for (int g = 0; g < G; ++g) {
-    const size_t qrow = ((size_t)w.b * p.H + w.h * G + g) * p.L;
-    for (int qt = lo; qt < hi; ++qt) {
-      const int t0 = qt * kT;
-      __syncthreads();
-      stage<DK>(q_s, p.q, qrow, t0, len, p.in_dtype);
-      stage<DV>(do_s, p.dO, qrow, t0, len, p.out_dtype);
-      stage_rows(p, lse_s, delta_s, qrow, t0, len);
-      __syncthreads();
-      float P[4][4], dS[4][4];
-      grad_scores<DK, DV>(p, q_s, k_s, do_s, v_s, lse_s, delta_s, t0, j0, len, tx, ty, P, dS);
+  window::query_tiles<kT>(j0, min(j0 + kRows, len) - 1, len, p.window, p.n_sink, lo, hi);
+  const int per = hi - lo, all_items = per * G;  // (head of the group, query tile), query tiles fastest
+  const int first = is_cut ? (int)((long long)all_items * part / kp.parts) : 0;
+  const int last = is_cut ? (int)((long long)all_items * (part + 1) / kp.parts) : all_items;
+  stage<DK, kRows>(k_s, p.k, krow, j0, len, p.in_dtype);
+  stage<DV, kRows>(v_s, p.v, krow, j0, len, p.in_dtype);
+  const float c = p.scale * kLog2e;
+  const int j_w = j0 + warp * R;  // the warp's first key
+  float* pw_s = p_s + warp * R * kLP;
+  float* dw_s = ds_s + warp * R * kLP;
+  float dk[R][kVals<DK>] = {}, dv[R][kVals<DV>] = {};
+  for (int item = first; item < last; ++item) {
+    const int t0 = (lo + item % per) * kT;
+    const size_t qrow = ((size_t)b * p.H + h * G + item / per) * p.L;
+    __syncthreads();
+    stage<DK, kT>(q_s, p.q, qrow, t0, len, p.in_dtype);
+    stage<DV, kT>(do_s, p.dO, qrow, t0, len, p.out_dtype);
+    float lse[2], delta[2];  // of this lane's queries; behind the end every weight is zero
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p_s[(ty + 16 * i) * kLP + tx + 16 * j] = P[i][j];
-          ds_s[(ty + 16 * i) * kLP + tx + 16 * j] = dS[i][j];
-        }
-      __syncthreads();
-      cols_times_tile<DV>(dv, p_s, ty, do_s, tx);
-      cols_times_tile<DK>(dk, ds_s, ty, q_s, tx);
+    for (int n = 0; n < 2; ++n) {
+      const int t = t0 + lane + 32 * n;
+      lse[n] = t < len ? p.lse[qrow + t] * kLog2e : INFINITY;
+      delta[n] = t < len ? p.delta[qrow + t] : 0.f;
     }
+    __syncthreads();
+    float s[R][2], dp[R][2];
+    scores<DK, R>(s, k_s + warp * R * (DK + 4), q_s, lane);
+    scores<DV, R>(dp, v_s + warp * R * (DV + 4), do_s, lane);
+    const bool all = t0 >= j_w + R - 1 && (t0 + kT - 1 - j_w < p.window || j_w + R <= p.n_sink);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float P = exp2f(fmaf(s[i][n], c, -lse[n]));
+        if (!all && !window::visible(t0 + lane + 32 * n, j_w + i, p.window, p.n_sink)) P = 0.f;
+        pw_s[i * kLP + lane + 32 * n] = P;
+        dw_s[i * kLP + lane + 32 * n] = P == 0.f ? 0.f : P * (dp[i][n] - delta[n]);
+      }
+    __syncwarp();
+    products<DV, R>(dv, pw_s, do_s, lane);
+    products<DK, R>(dk, dw_s, q_s, lane);
+    __syncwarp();
+  }
+  if (is_cut) {  // [tile][part][dk, then dv] of the CTA's rows, fp32
+    float* out = kp.part + (((size_t)kp.head * kp.sinks + tile) * kp.parts + part) * kRows * (DK + DV);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      put_row<DK>(out, warp * R + i, dk[i], p.scale, lane, kF32);
+      put_row<DV>(out + kRows * DK, warp * R + i, dv[i], 1.f, lane, kF32);
+    }
+    return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = j0 + 4 * ty + i;
-    if (j >= len) continue;
-    put_row<DK>(p.dk, krow + j, dk[i], p.scale, tx, p.in_dtype);
-    put_row<DV>(p.dv, krow + j, dv[i], 1.f, tx, p.in_dtype);
+  for (int i = 0; i < R; ++i) {
+    if (j_w + i >= len) break;
+    put_row<DK>(p.dk, krow + j_w + i, dk[i], p.scale, lane, p.in_dtype);
+    put_row<DV>(p.dv, krow + j_w + i, dv[i], 1.f, lane, p.in_dtype);
   }
 }
 
-template <typename K>
-cudaError_t run(K kernel, size_t floats, long long ctas, const WindowArgs& p, cudaStream_t stream) {
+// The cut tiles' parts, added in their order; one value per thread.
+__global__ void __launch_bounds__(256) window_sum_parts_kernel(WindowArgs p, KeyPass kp, int rows, int dk, int dv) {
+  const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = rows * (dk + dv);
+  const size_t which = e / per;  // (sequence, k/v head, tile)
+  if (which >= (size_t)p.B * p.Hkv * kp.sinks) return;
+  int x = static_cast<int>(e % per);
+  const float* from = kp.part + which * kp.parts * per + x;
+  const bool keys = x < rows * dk;
+  if (!keys) x -= rows * dk;
+  const int d = keys ? dk : dv;
+  const size_t head = which / kp.sinks;
+  const int j = static_cast<int>(which % kp.sinks) * rows + x / d;
+  if (j >= window::seq_len(p, static_cast<int>(head / p.Hkv))) return;
+  float a = 0.f;
+  for (int i = 0; i < kp.parts; ++i) a += from[(size_t)i * per];
+  store_elem(keys ? p.dk : p.dv, (head * p.L + j) * d + x % d, a, p.in_dtype);
+}
+
+template <typename K, typename... A>
+cudaError_t run(K kernel, size_t floats, long long ctas, cudaStream_t stream, const A&... args) {
   const size_t smem = floats * sizeof(float);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(p);
+  kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(args...);
+  return cudaGetLastError();
+}
+
+constexpr int kSms = 148;
+long long row_tiles(const WindowArgs& p, int rows, int heads) { return (long long)p.B * heads * ((p.L + rows - 1) / rows); }
+
+template <int DK, int DV, int R>
+cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
+  constexpr int kRows = kWarps * R;
+  return run(window_fwd_kernel<DK, DV, R>, kRows * (DK + 4 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
+}
+
+template <int DK, int DV, int R>
+cudaError_t dq_pass(const WindowArgs& p, cudaStream_t stream) {
+  constexpr int kRows = kWarps * R;
+  return run(window_dq_kernel<DK, DV, R>, kRows * (DK + DV + 8 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
+}
+
+// Keys per CTA of the keys' pass, in units of the warps: 4 where 8 would leave SMs without a CTA.
+int key_rows(int B, int Hkv, int L) { return (long long)B * Hkv * ((L + 8 * kWarps - 1) / (8 * kWarps)) >= kSms ? 8 : 4; }
+
+// The keys' pass of a call: its sink tiles cut, or, where that leaves SMs without a CTA, the walk of every tile.
+template <int R>
+KeyPass cut(int B, int H, int Hkv, int L, int window, int n_sink) {
+  constexpr int kRows = kWarps * R;
+  KeyPass kp = window::key_pass<kRows, kT>(H, Hkv, L, window, n_sink);
+  const long long tiles = (L + kRows - 1) / kRows, heads = (long long)B * Hkv;
+  if (heads * (tiles + (long long)kp.sinks * (kp.parts - 1)) >= kSms) return kp;
+  const int near = (window + kRows - 2) / kT + 2, walk = (L + kT - 1) / kT;  // query tiles that see a tile's keys
+  const long long items = (long long)(H / Hkv) * (n_sink > 0 || near > walk ? walk : near);
+  const long long parts = kSms / (heads * tiles) < items ? kSms / (heads * tiles) : items;
+  if (parts >= 2) kp.sinks = static_cast<int>(tiles), kp.parts = static_cast<int>(parts);
+  return kp;
+}
+
+template <int DK, int DV, int R>
+cudaError_t keys_pass(const WindowArgs& p, cudaStream_t stream) {
+  constexpr int kRows = kWarps * R;
+  KeyPass kp = cut<R>(p.B, p.H, p.Hkv, p.L, p.window, p.n_sink);
+  kp.part = static_cast<float*>(p.scratch) + ((size_t)p.B * p.H * p.L + 63) / 64 * 64;  // behind delta
+  const long long ctas = (long long)p.B * p.Hkv * kp.sinks * (kp.parts - 1) + row_tiles(p, kRows, p.Hkv);
+  const cudaError_t e = run(window_dkdv_kernel<DK, DV, R>, kRows * (DK + DV + 8 + 2 * kLP) + kT * (DK + DV + 8), ctas, stream, p, kp);
+  if (e != cudaSuccess || kp.sinks == 0) return e;
+  const size_t values = (size_t)p.B * p.Hkv * kp.sinks * kRows * (DK + DV);
+  window_sum_parts_kernel<<<(unsigned)((values + 255) / 256), 256, 0, stream>>>(p, kp, kRows, DK, DV);
   return cudaGetLastError();
 }
 
 template <int DK, int DV>
-cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
-  const long long tiles = (p.L + kT - 1) / kT;
-  return run(window_fwd_kernel<DK, DV>, kT * (2 * (DK + 4) + (DV + 4) + kLP), tiles * p.H * p.B, p, stream);
-}
-
-template <int DK, int DV>
 cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
-  const long long tiles = (p.L + kT - 1) / kT;
-  const size_t base = kT * (2 * (DK + 4) + 2 * (DV + 4) + 2);
-  const cudaError_t e = run(window_dq_kernel<DK, DV>, base + kT * kLP, tiles * p.H * p.B, p, stream);
+  const cudaError_t e = row_tiles(p, 8 * kWarps, p.H) >= kSms ? dq_pass<DK, DV, 8>(p, stream) : dq_pass<DK, DV, 4>(p, stream);
   if (e != cudaSuccess) return e;
-  return run(window_dkdv_kernel<DK, DV>, base + 2 * kT * kLP, tiles * p.Hkv * p.B, p, stream);
+  return key_rows(p.B, p.Hkv, p.L) == 8 ? keys_pass<DK, DV, 8>(p, stream) : keys_pass<DK, DV, 4>(p, stream);
 }
 
 template <typename F>
@@ -430,7 +497,17 @@ cudaError_t for_dim(int d, F f) {
 
 cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& p, cudaStream_t stream) {
   if (window_tc_supported(dk, dv, p.in_dtype)) return launch_window_attn_tc(dk, p, stream);
-  return for_dim(dk, [&](auto k) { return for_dim(dv, [&](auto v) { return forward<k(), v()>(p, stream); }); });
+  return for_dim(dk, [&](auto k) {
+    return for_dim(dv, [&](auto v) {
+      return row_tiles(p, 8 * kWarps, p.H) >= kSms ? forward<k(), v(), 8>(p, stream) : forward<k(), v(), 4>(p, stream);
+    });
+  });
+}
+
+size_t window_bwd_scratch_bytes(int B, int H, int Hkv, int L, int dk, int dv, int window, int n_sink) {
+  const int w = window < L ? window : L, s = n_sink < L ? n_sink : L, rows = key_rows(B, Hkv, L) * kWarps;
+  const KeyPass kp = rows == 8 * kWarps ? cut<8>(B, H, Hkv, L, w, s) : cut<4>(B, H, Hkv, L, w, s);
+  return (((size_t)B * H * L + 63) / 64 * 64 + (size_t)B * Hkv * kp.sinks * kp.parts * rows * (dk + dv)) * sizeof(float);
 }
 
 cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& p, cudaStream_t stream) {

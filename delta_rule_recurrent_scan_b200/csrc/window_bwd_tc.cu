@@ -17,8 +17,7 @@
 // A warpgroup takes half of a tile's columns: thread = (lane, half).  One load warp (TMA rings of two slots), one warp
 // whose first lane issues the products.  Rows behind a sequence's end are zeroed in shared memory.
 //
-// The key tiles that hold sinks are seen by every later query.  Where there are one or two of them their walk is cut
-// into parts of a regular tile's length; the parts' fp32 sums go to the workspace and a last launch adds them in order.
+// Key tiles with sinks may be cut into parts (window::key_pass); part: [B, Hkv, sinks, parts, 2, 128, D].
 #include "window_tc.cuh"
 
 namespace kdn {
@@ -80,12 +79,6 @@ __global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* 
 }
 
 // ------------------------------------------------------------------------------------------ dk, dv
-struct KeyPass {
-  int sinks;   // key tiles whose walk is cut
-  int parts;   // into this many parts
-  float* part; // [B, Hkv, sinks, parts, 2, 128, D]
-};
-
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     window_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -101,20 +94,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
-  // the cut walks come first (they are the longest), then the other key tiles
-  unsigned x = blockIdx.x;
-  const unsigned cut = (unsigned)bh * kp.sinks * kp.parts;
-  int tile, part = 0, y;
-  const bool is_cut = x < cut;
-  if (is_cut) {
-    part = x % kp.parts, x /= kp.parts;
-    tile = x % kp.sinks, y = x / kp.sinks;
-  } else {
-    x -= cut;
-    const int rest = tiles - kp.sinks;
-    tile = kp.sinks + x % rest, y = x / rest;
-  }
-  const int kvh = y % p.Hkv, b = y / p.Hkv;
+  int part;
+  const bool is_cut = window::key_tile_of(kp, bh, tiles, blockIdx.x, part);
+  const int tile = kp.tile, kvh = kp.head % p.Hkv, b = kp.head / p.Hkv;
   const int len = window::seq_len(p, b), j0 = tile * kT;
   if (p.zero_rest && part == 0 && j0 + kT > len) {
     const size_t row0 = (size_t)(b * p.Hkv + kvh) * p.L;
@@ -628,21 +610,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// One or two sink tiles: cut their walk (every later query tile) into parts of a regular tile's walk.
-KeyPass key_pass(int H, int Hkv, int L, int window, int n_sink) {
-  const int tiles = (L + kT - 1) / kT, sinks = n_sink > 0 ? (n_sink < L ? (n_sink - 1) / kT + 1 : tiles) : 0;
-  KeyPass kp{0, 1, nullptr};
-  if (sinks == 0 || sinks > 2 || sinks >= tiles) return kp;
-  const int regular = (window - 1) / kT + 2;  // query tiles that see a tile within the window
-  int parts = (tiles + regular - 1) / regular;
-  const int items = tiles * (H / Hkv);
-  if (parts > 64) parts = 64;
-  if (parts > items / 4) parts = items / 4;  // a part shorter than four tiles is all start-up
-  if (parts < 2) return kp;
-  kp.sinks = sinks, kp.parts = parts;
-  return kp;
-}
-
 struct Layout {
   size_t rows, dO, part, end;  // byte offsets in the scratch
 };
@@ -657,7 +624,7 @@ Layout layout(int B, int H, int Hkv, int L, int D, int out_dtype, const KeyPass&
 
 template <int D>
 cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
-  KeyPass kp = key_pass(p.H, p.Hkv, p.L, p.window, p.n_sink);
+  KeyPass kp = window::key_pass<kT, kT>(p.H, p.Hkv, p.L, p.window, p.n_sink);
   const Layout l = layout(p.B, p.H, p.Hkv, p.L, D, p.out_dtype, kp);
   char* scratch = static_cast<char*>(p.scratch);
   float2* rows = reinterpret_cast<float2*>(scratch + l.rows);
@@ -698,7 +665,7 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
 }  // namespace
 
 size_t window_bwd_tc_scratch_bytes(int B, int H, int Hkv, int L, int d, int out_dtype, int window, int n_sink) {
-  return layout(B, H, Hkv, L, d, out_dtype, key_pass(H, Hkv, L, window < L ? window : L, n_sink < L ? n_sink : L)).end;
+  return layout(B, H, Hkv, L, d, out_dtype, window::key_pass<kT, kT>(H, Hkv, L, window < L ? window : L, n_sink < L ? n_sink : L)).end;
 }
 
 cudaError_t launch_window_bwd_tc(int d, const WindowArgs& p, cudaStream_t stream) {

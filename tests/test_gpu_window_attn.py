@@ -98,22 +98,22 @@ def test_shared_heads(H, Hkv, dtype):
     _check(*_inputs(2, H, Hkv, 300, 64, 64, dtype, seed=5), 90, 9)
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.bfloat16, 64), (torch.bfloat16, 128)])
 @pytest.mark.parametrize("n_sink", [1, 128, 200, 300])
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (4, 2)])
-def test_sinks_of_a_long_sequence(d, n_sink, H, Hkv):
+def test_sinks_of_a_long_sequence(dtype, d, n_sink, H, Hkv):
     """One or two sink tiles whose walk over the later queries is cut into parts (and three, where it is not), in a
     batch whose shorter sequences leave some parts empty."""
     lens = torch.tensor([1700, 1700, 130, 0], dtype=torch.int32, device=DEV)
-    _check(*_inputs(4, H, Hkv, 1700, d, d, torch.bfloat16, seed=16), 60, n_sink, lens)
+    _check(*_inputs(4, H, Hkv, 1700, d, d, dtype, seed=16), 60, n_sink, lens)
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.float32, 16), (torch.bfloat16, 64), (torch.bfloat16, 128)])
 @pytest.mark.parametrize("B,H,Hkv", [(5, 12, 4), (7, 7, 7)])
-def test_more_work_than_multiprocessors(d, B, H, Hkv):
+def test_more_work_than_multiprocessors(dtype, d, B, H, Hkv):
     """Every CTA takes several works in turn, of sequences of all lengths."""
     lens = torch.tensor([900, 0, 513, 1, 256, 899, 128][:B], dtype=torch.int32, device=DEV)
-    _check(*_inputs(B, H, Hkv, 900, d, d, torch.bfloat16, seed=17), 200, 20, lens)
+    _check(*_inputs(B, H, Hkv, 900, d, d, dtype, seed=17), 200, 20, lens)
 
 
 @pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.bfloat16, 64), (torch.bfloat16, 128)])
