@@ -61,6 +61,16 @@ __host__ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int windo
   return k;
 }
 
+// Whether the backward makes these queries' delta from the weights instead of from o, in a sweep of its own.  dO . o with o
+// rounded to bf16 is off by about 2^-9 |dO| |o|, the same for all keys of a row; against P (dP - delta) that is
+// 1 / sqrt(n - 1) of what rounding dS costs for n keys of equal weight, so it shows where rows see few keys (the first
+// rows of every sequence hold a third of the gradient's energy: 1.5 times the error of the rounded result instead of
+// 1.4), and there the walk is short.  Up to 256 keys, in tiles of T.
+template <int T>
+__host__ __device__ __forceinline__ bool exact_delta(const WindowArgs& p, const KeyTiles& k) {
+  return p.out_dtype == kBF16 && (k.hi - k.lo) * T <= 256;
+}
+
 // Query tiles (of T tokens) of a sequence of len tokens that see a key of j0 .. j1: [lo, hi).
 template <int T>
 __host__ __device__ __forceinline__ void query_tiles(int j0, int j1, int len, int window, int n_sink, int& lo, int& hi) {

@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs p, int dv)
   if (lane == 0) p.delta[row] = x;
 }
 
-template <int DK, int DV, int R>
+// ROUNDED: o is bf16, and a first sweep may make delta = sum P dP, also for the keys' pass (window::exact_delta).
+template <int DK, int DV, int R, bool ROUNDED>
 __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
   constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
@@ -288,8 +289,22 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
     lse[i] = in ? p.lse[qrow + t_w + i] * kLog2e : 0.f;
     delta[i] = in ? p.delta[qrow + t_w + i] : 0.f;
   }
-  for (int it = 0; it < kt.count(); ++it) {
-    const int j0 = kt.walk(it) * kT;
+  const int n = kt.count(), before = ROUNDED && window::exact_delta<kT>(p, kt) ? n : 0;
+  float sum[R];
+  if constexpr (ROUNDED) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) sum[i] = 0.f;
+  }
+  for (int it = -before; it < n; ++it) {
+    const int j0 = kt.walk(it < 0 ? it + n : it) * kT;
+    if (ROUNDED && it == 0 && before > 0) {
+      reduce_rows<1>(sum);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        delta[i] = sum[i];
+        if (lane == 0 && t_w + i < len) p.delta[qrow + t_w + i] = sum[i];
+      }
+    }
     __syncthreads();
     stage<DK, kT>(k_s, p.k, krow, j0, len, p.in_dtype);
     stage<DV, kT>(v_s, p.v, krow, j0, len, p.in_dtype);
@@ -301,11 +316,15 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float P = exp2f(fmaf(s[i][n], c, -lse[i]));
-        w_s[i * kLP + lane + 32 * n] =
-            all || window::visible(t_w + i, j0 + lane + 32 * n, p.window, p.n_sink) ? P * (dp[i][n] - delta[i]) : 0.f;
+      for (int u = 0; u < 2; ++u) {
+        const float P = exp2f(fmaf(s[i][u], c, -lse[i]));
+        const bool seen = all || window::visible(t_w + i, j0 + lane + 32 * u, p.window, p.n_sink);
+        if (ROUNDED && it < 0)
+          sum[i] += seen ? P * dp[i][u] : 0.f;
+        else
+          w_s[i * kLP + lane + 32 * u] = seen ? P * (dp[i][u] - delta[i]) : 0.f;
       }
+    if (ROUNDED && it < 0) continue;
     __syncwarp();
     products<DK, R>(acc, w_s, k_s, lane);
     __syncwarp();
@@ -442,7 +461,7 @@ cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
 template <int DK, int DV, int R>
 cudaError_t dq_pass(const WindowArgs& p, cudaStream_t stream) {
   constexpr int kRows = kWarps * R;
-  return run(window_dq_kernel<DK, DV, R>, kRows * (DK + DV + 8 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
+  return run(p.out_dtype == kBF16 ? window_dq_kernel<DK, DV, R, true> : window_dq_kernel<DK, DV, R, false>, kRows * (DK + DV + 8 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
 }
 
 // Keys per CTA of the keys' pass, in units of the warps: 4 where 8 would leave SMs without a CTA.

@@ -364,6 +364,7 @@ struct QueryPass {
 };
 struct QueryWork {
   int b, kvh, qrow, t0, len, n;  // n = 0: nothing to do
+  int before;                    // key tiles of a first sweep: 0 or n
   KeyTiles kt;
 };
 __device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const QueryPass& qp, unsigned x) {
@@ -377,6 +378,7 @@ __device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const Query
   w.len = window::seq_len(p, b);
   w.kt = window::key_tiles<kT>(w.t0, min(w.t0 + kT, w.len) - 1, p.window, p.n_sink);
   w.n = w.t0 < w.len ? w.kt.count() : 0;
+  w.before = window::exact_delta<kT>(p, w.kt) ? w.n : 0;
   return w;
 }
 // The r-th work of this CTA: every other round runs backwards, so that long and short works meet.
@@ -384,17 +386,20 @@ __device__ __forceinline__ unsigned nth_work(unsigned r) {
   return r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+// A work may take two sweeps over its key tiles, the first for delta_t = sum_j P_tj dP_tj in fp32, which also replaces the
+// value from the rounded o for the keys' pass (window::exact_delta).
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     window_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, WindowArgs p,
-                        const float2* rows, QueryPass qp) {
+                        float2* rows, QueryPass qp) {
   using S = Smem<D>;
   constexpr int kNP = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready[2], done, last;
   __shared__ uint32_t tmem_base;
+  __shared__ float delta_s[2][kT];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -429,9 +434,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (x >= qp.works) continue;
         const QueryWork w = query_work(p, qp, x);
         const int row = w.b * p.Hkv + w.kvh;
-        for (int it = 0; it < w.n; ++it) {
+        const int steps = w.before + w.n;
+        for (int it = 0; it < steps; ++it) {
           const unsigned slot = nk & 1;
-          const int j0 = w.kt.walk(it) * kT;
+          const int j0 = w.kt.walk(it < w.n ? it : it - w.n) * kT;
           if (nk > 1) fine = sm100::mbar_wait_bounded(&k_empty[slot], ((nk >> 1) - 1) & 1, kWaitCycles);
           if (!fine) break;
           sm100::mbar_arrive_expect_tx(&k_full[slot], S::kTile);
@@ -468,7 +474,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (x >= qp.works) continue;
       const QueryWork w = query_work(p, qp, x);
       if (w.n == 0) continue;
-      // S and dP of the it-th tile, the c-th of this CTA: S is free once tile c - 1 is in registers.  k and v rows behind
+      const int steps = w.before + w.n;
+      // S and dP of the it-th step, the c-th of this CTA: S is free once step c - 1 is in registers.  k and v rows behind
       // the end are zeroed (their weights are zero).
       auto issue = [&](int it) {
         const unsigned slot = c & 1;
@@ -476,7 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                (c == 0 || warp_wait(&s_free, (c - 1) & 1));
         if (!fine) return;
         sm100::tc_fence_after();
-        const int inside = w.len - w.kt.walk(it) * kT;
+        const int inside = w.len - w.kt.walk(it < w.n ? it : it - w.n) * kT;
         if (inside < kT) {
           zero_rows<kNP>(sm + S::kRing + 2 * slot * S::kTile, inside, lane);
           zero_rows<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, inside, lane);
@@ -488,24 +495,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mma_rows<D>(t_dp + 128 * slot, do_desc, k_desc + (S::kTile >> 4));
           sm100::mma_commit(&dp_ready[slot]);
           sm100::mma_commit(&v_empty[slot]);
-          if (it + 1 == w.n) sm100::mma_commit(&q_empty);
+          if (it + 1 == steps) sm100::mma_commit(&q_empty);
         }
         ++c;
       };
       fine = warp_wait(&q_full, nq & 1);
       ++nq;
       if (fine) issue(0);
-      for (int it = 0; it < w.n && fine; ++it) {
-        const unsigned mine = c - 1, slot = mine & 1;  // tile ``it``
-        if (it + 1 < w.n) issue(it + 1);
+      for (int it = 0; it < steps && fine; ++it) {
+        const unsigned mine = c - 1, slot = mine & 1;  // step ``it``
+        if (it + 1 < steps) issue(it + 1);
         if (!fine) break;
         fine = warp_wait(&ds_ready[slot], (mine >> 1) & 1);
         if (!fine) break;
         sm100::tc_fence_after();
         if (lane == 0) {
-          mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring + 2 * slot * S::kTile), it > 0);
+          const int sweep = it - w.before;  // >= 0: the tile of the sweep that adds up dq
+          if (sweep >= 0) mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring + 2 * slot * S::kTile), sweep > 0);
           sm100::mma_commit(&k_empty[slot]);
-          if (it + 1 == w.n) sm100::mma_commit(&done);
+          if (it + 1 == steps) sm100::mma_commit(&done);
         }
       }
     }
@@ -529,9 +537,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int t = w.t0 + (tid & 127);
       const int w_first = w.t0 + 32 * (warp & 3), w_last = w_first + 31;
       const float2 row = t < w.len ? rows[(size_t)w.qrow * p.L + t] : make_float2(0.f, 0.f);
-      const float2 l2 = make_float2(row.x, row.x), d2 = make_float2(row.y, row.y);
-      for (int it = 0; it < w.n; ++it, ++c) {
-        const int j0 = w.kt.walk(it) * kT + 64 * half;
+      const float2 l2 = make_float2(row.x, row.x);
+      float2 d2 = make_float2(row.y, row.y), sum = make_float2(0.f, 0.f);
+      const int steps = w.before + w.n;
+      for (int it = 0; it < steps; ++it, ++c) {
+        const int j0 = w.kt.walk(it < w.n ? it : it - w.n) * kT + 64 * half;
         fine = warp_wait(&s_ready, c & 1);
         if (!fine) break;
         sm100::tc_fence_after();
@@ -564,6 +574,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!fine) break;
         sm100::tc_fence_after();
         const uint32_t t_mine = t_dp + 128 * (c & 1) + lanes + 64 * half;
+        if (it < w.before) {  // the first sweep
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float dp[32];
+            sm100::tmem_ld32(t_mine + 32 * u, dp);
+            sm100::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              sum = fma2(make_float2(s[u][e], s[u][e + 1]), make_float2(dp[e], dp[e + 1]), sum);
+          }
+          sm100::tc_fence_before();
+          warp_arrive(&ds_ready[c & 1]);
+          if (it + 1 == w.n) {  // the row's other half of the columns is the other warpgroup's
+            delta_s[half][tid & 127] = sum.x + sum.y;
+            chunk::named_sync(1, 256);
+            const float delta = delta_s[0][tid & 127] + delta_s[1][tid & 127];
+            d2 = make_float2(-delta, -delta);
+            if (half == 0 && t < w.len) rows[(size_t)w.qrow * p.L + t].y = -delta;
+            chunk::named_sync(1, 256);  // both have read it
+          }
+          continue;
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           float dp[32], q[16];
@@ -648,13 +680,15 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   e = cudaFuncSetAttribute(window_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long keys = (long long)bh * (kp.sinks * kp.parts + tiles - kp.sinks);
-  window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, kp);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   QueryPass qp;
   qp.works = (unsigned)((long long)p.B * p.H * tiles), qp.tiles = tiles;
   qp.group = make_divisor(p.H / p.Hkv), qp.kv_heads = make_divisor(p.Hkv), qp.batch = make_divisor(p.B);
-  window_dq_tc_kernel<D><<<qp.works < (unsigned)sms ? qp.works : (unsigned)sms, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, qp);
+  // the queries' pass first: it may replace the rows' delta
+  const unsigned ctas = qp.works < (unsigned)sms ? qp.works : (unsigned)sms;
+  window_dq_tc_kernel<D><<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, qp);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, kp);
   e = cudaGetLastError();
   if (e != cudaSuccess || kp.sinks == 0) return e;
   const size_t words = (size_t)bh * kp.sinks * 2 * kT * D / 8;
