@@ -521,6 +521,12 @@ def _stream_of(stream, dev):
     return stream.cuda_stream
 
 
+def _int32(x, name):
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -533,7 +539,8 @@ def _scratch(workspace, need, dev):
     return workspace
 
 
-def _window_args(q, k, v, lens, scale):
+def _window_args(q, k, v, lens, scale, window, n_sink):
+    _int32(window, "window"), _int32(n_sink, "n_sink")
     try:
         B, H, L, dk = q.shape
         _, Hkv, _, dv = v.shape
@@ -563,7 +570,7 @@ def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=No
     h // (H / kv_heads).  lens [B] int32 (or None): tokens of each sequence; rows behind them are left as they were
     in the given o and lse, and are zero in those allocated here.  scale defaults to 1 / sqrt(d_k), out_dtype to q's.
     Returns (o [B,H,L,d_v], lse [B,H,L] fp32)."""
-    B, H, Hkv, L, dk, dv, dev, scale = _window_args(q, k, v, lens, scale)
+    B, H, Hkv, L, dk, dv, dev, scale = _window_args(q, k, v, lens, scale, window, n_sink)
     out_dtype = out_dtype or (q.dtype if o is None else o.dtype)
     if out_dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {out_dtype}")
@@ -596,7 +603,7 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
     """Gradients of window_attn for upstream dO (of o's type), from its inputs and its o and lse.  Returns a dict with
     dq, dk, dv in q's type (dk and dv summed over the heads that share them); rows behind a sequence's last token are
     left as they were in given tensors, and are zero in those allocated here."""
-    B, H, Hkv, L, d_k, d_v, dev, scale = _window_args(q, k, v, lens, scale)
+    B, H, Hkv, L, d_k, d_v, dev, scale = _window_args(q, k, v, lens, scale, window, n_sink)
     dtype = q.dtype
     if o.dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {o.dtype}")
@@ -628,13 +635,17 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
 class Pages:
     """The books of a paged cache (kdn_pages): table [rows, max_pages], lens [rows] and refs [num_pages], int32.  One
     set serves every layer; a layer's pages are k_pages [num_pages, kv_heads, page_size, d_k] and v_pages.
-    ``workspace`` (allocated at the first call) holds the status of the last book-keeping call:
+    ``workspace`` (allocated with the books) holds the status of the last book-keeping call:
     read_device_status(pages.workspace)."""
     table: torch.Tensor
     lens: torch.Tensor
     refs: torch.Tensor
     page_size: int
     workspace: torch.Tensor | None = None
+
+    def __post_init__(self):
+        if self.workspace is None and self.table.is_cuda:
+            self.workspace = _scratch(None, lib().kdn_pages_workspace_bytes(self._c()), self.table.device)
 
     def _c(self, dev=None):
         table, lens, refs = self.table, self.lens, self.refs
@@ -661,22 +672,20 @@ def _list(t, name, dev):
     return _need(t, name, t.shape, torch.int32, dev)
 
 
-def _books(pages, stream):
+def _books(pages):
     c = pages._c()
-    dev = pages.table.device
-    if pages.workspace is None:
-        with _on(stream):
-            pages.workspace = _scratch(None, lib().kdn_pages_workspace_bytes(ctypes.byref(c)), dev)
-    return c, dev, pages.workspace
+    return c, pages.table.device, pages.workspace
 
 
 def pages_reserve(pages, rows, counts, stream=None):
     """Adds tokens to the listed rows (int32 [n]), with the pages they need: ``counts`` each, or counts[i] (int32 [n])."""
-    c, dev, ws = _books(pages, stream)
+    c, dev, ws = _books(pages)
     _list(rows, "rows", dev)
     each = isinstance(counts, torch.Tensor)
     if each:
         _need(counts, "counts", rows.shape, torch.int32, dev)
+    else:
+        _int32(counts, "counts")
     st = lib().kdn_pages_reserve(c, rows.numel(), _at(rows), _at(counts) if each else None,
                                  0 if each else counts, _at(ws), ws.numel(), _stream_of(stream, dev))
     if st:
@@ -686,7 +695,7 @@ def pages_reserve(pages, rows, counts, stream=None):
 def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
     """Makes each empty row dst_rows[i] a copy of src_rows[i], sharing its full pages.  Returns moves [n, 2] int32, the
     part-filled pages that pages_copy has to copy (in every layer) before the rows are used."""
-    c, dev, ws = _books(pages, stream)
+    c, dev, ws = _books(pages)
     _list(src_rows, "src_rows", dev)
     _need(dst_rows, "dst_rows", src_rows.shape, torch.int32, dev)
     with _on(stream):
@@ -702,7 +711,7 @@ def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
 
 def pages_free(pages, rows, stream=None):
     """Empties the listed rows; pages that no row names any more are free."""
-    c, dev, ws = _books(pages, stream)
+    c, dev, ws = _books(pages)
     _list(rows, "rows", dev)
     st = lib().kdn_pages_free(c, rows.numel(), _at(rows), _at(ws), ws.numel(), _stream_of(stream, dev))
     if st:
@@ -712,7 +721,7 @@ def pages_free(pages, rows, stream=None):
 def pages_compact(pages, moves=None, stream=None):
     """Moves the pages in use to the lowest page numbers.  Returns moves [num_pages // 2, 2] int32 for pages_copy (in
     every layer), ending in pairs of -1."""
-    c, dev, ws = _books(pages, stream)
+    c, dev, ws = _books(pages)
     with _on(stream):
         if moves is None:
             moves = torch.empty(c.num_pages // 2, 2, dtype=torch.int32, device=dev)
@@ -779,6 +788,7 @@ def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sin
     -inf, a broken table entry NaN."""
     num, Hkv, page, dk, dv = _pool(k_pages, v_pages)
     dev = k_pages.device
+    _int32(window, "window"), _int32(n_sink, "n_sink")
     if q.dim() != 3:
         raise ValueError("q must be [n, H, d_k]")
     n, H = q.shape[:2]

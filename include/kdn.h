@@ -23,6 +23,10 @@
  *                         Networks, Abstract)
  *   kdn_decode_step       one token against a resident state (delta or diag)
  *
+ * Beside them stands softmax attention over recent tokens, which such layers are mixed with: kdn_window_attn (and its
+ * backward) over whole sequences, kdn_paged_attn_step for one new token against a paged key-value cache, and the
+ * kdn_pages_* calls that keep that cache.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Pointers.  Every array argument is a DEVICE pointer (cudaMalloc, a CUDA
@@ -291,7 +295,8 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * q [B,H,L,d_k], k [B,kv_heads,L,d_k], v [B,kv_heads,L,d_v] (dims->in_dtype): query head h reads k/v head
  * h / (H / kv_heads); kv_heads divides H.  lens [B] int32 or NULL (= L): tokens of each sequence, held to
  * [0, L]; what memory holds behind a sequence's last token takes no part (it may be NaN), and its rows of o
- * and lse are left as they were (zero_rest = 0) or set to zero (1).  window >= 1 (>= L: plain causal attention), n_sink >= 0, scale > 0.
+ * and lse are left as they were (zero_rest = 0) or set to zero (1).  window >= 1 (>= L: plain causal attention), n_sink >= 0, 0 < scale <= 1e30.
+ * The sequences' own tokens must be finite: a hidden token's weight is 0, and 0 times its value has to be 0.
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
  * enter the second product as bf16; sums, maxima and both products' accumulators are fp32), everything else
@@ -307,7 +312,8 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  * delta_t = dO_t . o_t, P_tj = exp(scale q_t . k_j - lse_t) and dS_tj = P_tj (dO_t . v_j - delta_t):
  *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
  * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
- * gradients do not change from run to run.  Rows behind a sequence's last token are left as they were or set to
+ * gradients do not change from run to run.  Where rows see few keys and o is bf16, delta is made from P and dP
+ * instead of the rounded o.  Rows behind a sequence's last token are left as they were or set to
  * zero (zero_rest), in all three; lse has no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
                                     const void* v, const int* lens, int zero_rest, int window, int n_sink, float scale,
@@ -368,7 +374,8 @@ KDN_EXPORT kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int
 
 /* Writes the newest tokens of rows rows[0..n) into one layer's pages, after kdn_pages_reserve has added them:
  * k_new [n, kv_heads, tokens, d_k], v_new [n, kv_heads, tokens, d_v]; of entry i the first counts[i] (NULL: tokens)
- * are the last counts[i] tokens of the row.  Entries whose row, count or page is out of range are skipped. */
+ * are the last counts[i] tokens of the row.  Entries whose row, count or page is out of range are skipped; of a row
+ * listed twice either entry may be the one that stays. */
 KDN_EXPORT kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens,
                            int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new,
                            void* k_pages, void* v_pages, void* stream);

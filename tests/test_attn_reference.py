@@ -155,3 +155,10 @@ def test_books_oracle_keeps_its_counts():
     assert b.reserve([2], [40]) == "capacity"
     assert b.compact()[0] == (5, 2)
     count()
+
+
+def test_binding_refuses_numbers_beyond_32_bits():
+    x = torch.zeros(1, 2, 4, 16)
+    for bad in (dict(window=2**31), dict(window=4, n_sink=2**32 + 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            kdn.window_attn(x, x, x, **bad)
