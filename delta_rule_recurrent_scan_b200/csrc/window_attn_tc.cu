@@ -271,10 +271,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int u = 0; u < 4; ++u) {  // 32 columns: seen by every row of the warp, by none, or by some
             const int j = j0 + 32 * u;
             if (j + 31 <= w_first && (w_last - j < p.window || j + 32 <= p.n_sink)) continue;
-            const int hi = t - j, lo = hi - p.window, sinks = p.n_sink - j;  // visible: e <= hi, (e > lo or e < sinks)
+            const uint32_t seen = seen_bits(t - j, p.window, p.n_sink - j);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (e > hi || (e <= lo && e >= sinks)) s[u][e] = -INFINITY;
+              if (!(seen >> e & 1u)) s[u][e] = -INFINITY;
           }
         }
         float top[4];

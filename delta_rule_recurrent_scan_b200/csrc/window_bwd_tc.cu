@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int u = 0; u < 2; ++u) {  // 32 queries: all of them see the warp's keys, or some do
           const int q0 = t0 + 32 * u;
           if (q0 >= j_last && (q0 + 31 - j_first < p.window || j_last < p.n_sink)) continue;
-          const int near = j - q0, far = near + p.window;
+          const uint32_t seen = seeing_bits(j - q0, p.window, sink);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (e < near || (e >= far && !sink)) s[u][e] = 0.f;
+            if (!(seen >> e & 1u)) s[u][e] = 0.f;
         }
       }
 #pragma unroll
@@ -564,10 +564,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int u = 0; u < 2; ++u) {  // 32 keys: all of the warp's rows see them, or some do
             const int k0 = j0 + 32 * u;
             if (k0 + 31 <= w_first && (w_last - k0 < p.window || k0 + 32 <= p.n_sink)) continue;
-            const int hi = t - k0, lo = hi - p.window, sinks = p.n_sink - k0;
+            const uint32_t seen = seen_bits(t - k0, p.window, p.n_sink - k0);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (e > hi || (e <= lo && e >= sinks)) s[u][e] = 0.f;
+              if (!(seen >> e & 1u)) s[u][e] = 0.f;
           }
         }
         fine = warp_wait(&dp_ready[c & 1], (c >> 1) & 1);

@@ -42,6 +42,17 @@ __device__ __forceinline__ void zero_tile(void* dst, size_t row0, int row_bytes,
     static_cast<uint4*>(dst)[(row0 + first) * words + e] = make_uint4(0, 0, 0, 0);
 }
 
+// Bit e: whether a query ``back`` tokens behind the first of 32 keys sees the e-th of them; ``sinks`` of the keys are sinks.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }  // bits 0 .. n - 1
+__device__ __forceinline__ uint32_t seen_bits(int back, int window, int sinks) {
+  return below(back + 1) & (~below(back - window + 1) | below(sinks));
+}
+
+// Bit e: whether the e-th of 32 queries sees a key that lies ``ahead`` tokens behind the first of them (< 0: before it).
+__device__ __forceinline__ uint32_t seeing_bits(int ahead, int window, bool sink) {
+  return ~below(ahead) & (sink ? ~0u : below(ahead + window));
+}
+
 // One arrival for a warp, after all its lanes' work (32 single arrivals on one word take turns).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();

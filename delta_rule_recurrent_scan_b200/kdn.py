@@ -585,7 +585,8 @@ def window_attn(q, k, v, window, n_sink=0, lens=None, scale=None, o=None, lse=No
         new = torch.empty if lens is None or fresh else torch.zeros
         with _on(stream):
             if o is None:
-                o = new((B, H, L, dv), dtype=out_dtype, device=dev)
+                o = torch.empty_like(q) if new is torch.empty and dv == dk and out_dtype == q.dtype else \
+                    new((B, H, L, dv), dtype=out_dtype, device=dev)
             if lse is None:
                 lse = new((B, H, L), dtype=torch.float32, device=dev)
     if workspace is not None:
@@ -809,7 +810,8 @@ def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sin
     c = PagesC(num, page, table.shape[0], table.shape[1], table.data_ptr(), lens.data_ptr(), None)
     with _on(stream):
         if o is None:
-            o = torch.empty((n, H, dv), dtype=out_dtype, device=dev)
+            o = torch.empty_like(q) if dv == dk and out_dtype == q.dtype else \
+                torch.empty((n, H, dv), dtype=out_dtype, device=dev)
         if lse is None:
             lse = torch.empty((n, H), dtype=torch.float32, device=dev)
         need = lib().kdn_paged_step_workspace_bytes(c, n, H, Hkv, dk, dv, _DTYPES[q.dtype], window, n_sink)
