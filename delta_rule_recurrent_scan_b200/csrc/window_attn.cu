@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs p, int dv)
   if (lane == 0) p.delta[row] = x;
 }
 
-// ROUNDED: o is bf16, and a first sweep may make delta = sum P dP, also for the keys' pass (window::exact_delta).
-template <int DK, int DV, int R, bool ROUNDED>
+// A first sweep may make delta = sum P dP, also for the keys' pass (window::exact_delta).
+template <int DK, int DV, int R>
 __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
   constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
@@ -289,15 +289,13 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
     lse[i] = in ? p.lse[qrow + t_w + i] * kLog2e : 0.f;
     delta[i] = in ? p.delta[qrow + t_w + i] : 0.f;
   }
-  const int n = kt.count(), before = ROUNDED && window::exact_delta<kT>(p, kt) ? n : 0;
+  const int n = kt.count(), before = window::exact_delta<kT>(p, kt, t0) ? n : 0;
   float sum[R];
-  if constexpr (ROUNDED) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) sum[i] = 0.f;
-  }
+  for (int i = 0; i < R; ++i) sum[i] = 0.f;
   for (int it = -before; it < n; ++it) {
     const int j0 = kt.walk(it < 0 ? it + n : it) * kT;
-    if (ROUNDED && it == 0 && before > 0) {
+    if (it == 0 && before > 0) {
       reduce_rows<1>(sum);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -317,14 +315,14 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float P = exp2f(fmaf(s[i][u], c, -lse[i]));
+        const float P = window::sees_one_key(p, t_w + i) ? 1.f : exp2f(fmaf(s[i][u], c, -lse[i]));
         const bool seen = all || window::visible(t_w + i, j0 + lane + 32 * u, p.window, p.n_sink);
-        if (ROUNDED && it < 0)
+        if (it < 0)
           sum[i] += seen ? P * dp[i][u] : 0.f;
         else
           w_s[i * kLP + lane + 32 * u] = seen ? P * (dp[i][u] - delta[i]) : 0.f;
       }
-    if (ROUNDED && it < 0) continue;
+    if (it < 0) continue;
     __syncwarp();
     products<DK, R>(acc, w_s, k_s, lane);
     __syncwarp();
@@ -461,7 +459,7 @@ cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
 template <int DK, int DV, int R>
 cudaError_t dq_pass(const WindowArgs& p, cudaStream_t stream) {
   constexpr int kRows = kWarps * R;
-  return run(p.out_dtype == kBF16 ? window_dq_kernel<DK, DV, R, true> : window_dq_kernel<DK, DV, R, false>, kRows * (DK + DV + 8 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
+  return run(window_dq_kernel<DK, DV, R>, kRows * (DK + DV + 8 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
 }
 
 // Keys per CTA of the keys' pass, in units of the warps: 4 where 8 would leave SMs without a CTA.

@@ -378,7 +378,7 @@ __device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const Query
   w.len = window::seq_len(p, b);
   w.kt = window::key_tiles<kT>(w.t0, min(w.t0 + kT, w.len) - 1, p.window, p.n_sink);
   w.n = w.t0 < w.len ? w.kt.count() : 0;
-  w.before = window::exact_delta<kT>(p, w.kt) ? w.n : 0;
+  w.before = window::exact_delta<kT>(p, w.kt, w.t0) ? w.n : 0;
   return w;
 }
 // The r-th work of this CTA: every other round runs backwards, so that long and short works meet.
@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int w_first = w.t0 + 32 * (warp & 3), w_last = w_first + 31;
       const float2 row = t < w.len ? rows[(size_t)w.qrow * p.L + t] : make_float2(0.f, 0.f);
       const float2 l2 = make_float2(row.x, row.x);
+      const bool one = window::sees_one_key(p, t);
       float2 d2 = make_float2(row.y, row.y), sum = make_float2(0.f, 0.f);
       const int steps = w.before + w.n;
       for (int it = 0; it < steps; ++it, ++c) {
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t seen = seen_bits(t - k0, p.window, p.n_sink - k0);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(seen >> e & 1u)) s[u][e] = 0.f;
+              s[u][e] = !(seen >> e & 1u) ? 0.f : one ? 1.f : s[u][e];
           }
         }
         fine = warp_wait(&dp_ready[c & 1], (c >> 1) & 1);

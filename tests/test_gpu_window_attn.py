@@ -188,6 +188,20 @@ def test_gradient_error_where_rows_see_few_keys(L, window, n_sink, d):
         assert off <= ((2.0 if d >= 64 else 1.0) ** 0.5 + 0.1) * rounded, name
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 16), (torch.float32, 32), (torch.float32, 128), (torch.bfloat16, 32),
+                                     (torch.bfloat16, 64), (torch.bfloat16, 128)])
+@pytest.mark.parametrize("L,window", [(1, 5), (300, 1)])
+def test_a_softmax_over_one_key_has_no_gradient(L, window, dtype, d):
+    """dq and dk are exactly zero, dv is dO summed over the heads that share it (its weights are within 2 u |s| of 1)."""
+    q, k, v, dO = _inputs(2, 4, 2, L, d, d, dtype, seed=21)
+    for out_dtype in (torch.float32, torch.bfloat16):
+        o, lse, g = _check(q, k, v, dO, window, 0, out_dtype=out_dtype)
+        assert bool((g["dq"] == 0).all()) and bool((g["dk"] == 0).all())
+    # the first row of a longer sequence, next to rows that do have a gradient
+    q, k, v, dO = _inputs(1, 2, 1, 80, d, d, dtype, seed=22)
+    assert bool((_check(q, k, v, dO, 60, 3)[2]["dq"][:, :, 0] == 0).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_runs_are_equal_bit_for_bit(dtype):
     q, k, v, dO = _inputs(2, 6, 2, 900, 64, 64, dtype, seed=10)
