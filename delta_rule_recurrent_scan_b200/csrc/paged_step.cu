@@ -45,43 +45,83 @@ __device__ __forceinline__ float* part_sum(const PagedStepArgs& p, int dv) {
   return part_max(p, dv) + (size_t)p.n * p.H * p.splits;
 }
 
-// ------------------------------------------------------------------------------------------ fp32 CUDA cores
-// Every size and type.  128 threads, 8 query heads, tiles of 32 tokens staged as fp32: warp w has the scores of heads
-// 2 w and 2 w + 1 for its lane's token; then thread t has column t % d_v of every head's o.
-constexpr int kTok = 32, kThr = 128, kHB = 8;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int D>
-__device__ __forceinline__ bool stage_tokens(float* dst, const void* pool, const PagedStepArgs& p, const int* entries, int kvh,
-                                             int j0, int n, int win) {
-  constexpr int Q = D / 4;
-  bool bad = false;
-  for (int e = threadIdx.x; e < kTok * Q; e += kThr) {
-    const int r = e / Q, c = 4 * (e % Q), j = j0 + r;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j < n && window::visible(n - 1, j, win, p.n_sink)) {  // the pages of hidden tokens are not asked for
-      const int page = entries[j / p.page_size];
-      if (page < 0 || page >= p.num_pages) {
-        bad = true;
-      } else {
-        const size_t at = (((size_t)page * p.Hkv + kvh) * p.page_size + j % p.page_size) * D + c;
-        if (p.in_dtype == kBF16) {
-          const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(pool) + at);
-          x = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                          __uint_as_float(u.y & 0xffff0000u));
-        } else {
-          x = *reinterpret_cast<const float4*>(static_cast<const float*>(pool) + at);
-        }
-      }
-    }
-    *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x;
+// ------------------------------------------------------------------------------------------ fp32 CUDA cores
+// Every size and type, kHB = 8, 4 or 2 query heads per CTA.  Each of 4 warps walks units of 8 or 16 tokens with its own running maximum,
+// sum and o.  A lane holds 4 coordinates: d / 4 lanes read a token's key as one run of 16-byte words, 128 / d tokens at a
+// time, straight into registers; the next unit's keys are in flight while this one's values are used.
+//   scores:  4 multiply-adds per lane, token and head, then an exchange over the lanes of a token that halves the number
+//            of values with every step, so that 8 tokens cost 9 shuffles per head (40 one by one), leaving a lane with one
+//            token's scores;
+//   weights: the maxima move only when some score has outgrown them by 2^8 (one vote per unit); the 8 heads' weights go
+//            through 16 or 32 bytes of the warp's own shared memory per token;
+//   values:  o[8][4] += weight x value, the weights as broadcast reads.
+// About 110 instructions per token and warp against 1 KB of fp32 keys and values (d = 128).
+constexpr int kWarps = 4, kThr = 32 * kWarps;
+constexpr float kSlack = 8.f;  // growth of a maximum (base 2) that weights may keep
+
+// Four coordinates of a key or value.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<float> {
+  float4 x;
+  __device__ __forceinline__ void zero() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) { x = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ float4 get() const { return x; }
+};
+template <>
+struct Quad<__nv_bfloat16> {
+  uint2 x;
+  __device__ __forceinline__ void zero() { x = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = __ldcs(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
   }
-  return bad;
+};
+
+// Sums of N values over LANES neighbouring lanes, halving their number with every step while there are several: lane l is
+// left with the sum of value ``index``.
+template <int N, int LANES>
+__device__ __forceinline__ float fold(float (&x)[N], int lane, int& index) {
+  index = 0;
+  int n = N;
+#pragma unroll
+  for (int k = LANES / 2; k >= 1; k >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = (lane & k) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= n) break;
+        const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, k);
+      }
+      index += up ? n : 0;
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], k);
+    }
+  }
+  return x[0];
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kThr) paged_step_kernel(PagedStepArgs p) {
-  __shared__ __align__(16) float k_s[kTok * (DK + 4)], v_s[kTok * (DV + 4)], q_s[kHB * DK], p_s[kTok * kHB];
-  __shared__ float keep_s[kHB], l_s[kHB], m_s[kHB];
+template <int DK, int DV, int kHB, typename T>
+__global__ void __launch_bounds__(kThr, 2) paged_step_kernel(PagedStepArgs p) {
+  constexpr int kU = (DK > DV ? DK : DV) > 64 ? 8 : 16;       // tokens of a unit
+  constexpr int kKL = DK / 4, kVL = DV / 4;                   // lanes of a key, of a value
+  constexpr int kKT = 32 / kKL, kVT = 32 / kVL;               // tokens read at a time
+  constexpr int kKN = kU / kKT > 0 ? kU / kKT : 1, kVN = kU / kVT > 0 ? kU / kVT : 1;
+  static_assert(kKN * kKT >= kU && kVN * kVT >= kU, "a unit is covered");
+  __shared__ __align__(16) float p_s[kWarps][kKN * kKT > kVN * kVT ? kKN * kKT : kVN * kVT][kHB];
+  __shared__ __align__(16) float o_s[kWarps][kHB][DV];
+  __shared__ float l_s[kWarps][kHB], m_s[kWarps][kHB];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Part w = which<kHB>(p);
   if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -95,90 +135,177 @@ __global__ void __launch_bounds__(kThr) paged_step_kernel(PagedStepArgs p) {
   }
   const int win = p.window > 0 ? p.window : INT_MAX;
   KeyTiles kt{0, 0, 0};
-  if (n > 0) kt = window::key_tiles<kTok>(n - 1, n - 1, win, p.n_sink);
-  const int it0 = (int)((long long)kt.count() * w.split / p.splits), it1 = (int)((long long)kt.count() * (w.split + 1) / p.splits);
-  for (int e = tid; e < kHB * DK; e += kThr)
-    q_s[e] = e / DK < w.nh ? load_elem(p.q, ((size_t)w.b * p.H + w.h0) * DK + e, p.in_dtype) * p.scale : 0.f;
-  constexpr int kGroups = kThr / DV;  // token groups of the second half (d_v < 128)
-  const int col = tid % DV, tg = tid / DV;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[kHB] = {};
-  for (int it = it0; it < it1; ++it) {
-    const int j0 = kt.walk(it) * kTok;
-    __syncthreads();
-    bad |= stage_tokens<DK>(k_s, p.k_pages, p, entries, w.kvh, j0, n, win);
-    bad |= stage_tokens<DV>(v_s, p.v_pages, p, entries, w.kvh, j0, n, win);
-    __syncthreads();
-    float s[2] = {0.f, 0.f};
-#pragma unroll 8
-    for (int c = 0; c < DK; c += 4) {
-      const float4 k = *reinterpret_cast<const float4*>(k_s + lane * (DK + 4) + c);
+  if (n > 0) kt = window::key_tiles<kU>(n - 1, n - 1, win, p.n_sink);
+  const int u0 = (int)((long long)kt.count() * w.split / p.splits) + warp;
+  const int u1 = (int)((long long)kt.count() * (w.split + 1) / p.splits);
+  const T* kp = static_cast<const T*>(p.k_pages);
+  const T* vp = static_cast<const T*>(p.v_pages);
+  const int shift = 31 - __clz(p.page_size), mask = p.page_size - 1;
+
+  // a visible token's place in the pages, in tokens; -1: not to be read
+  auto place = [&](int j) -> long long {
+    if (j >= n || !window::visible(n - 1, j, win, p.n_sink)) return -1;
+    const int page = entries[j >> shift];
+    if (page < 0 || page >= p.num_pages) {
+      bad = true;
+      return -1;
+    }
+    return (((long long)page * p.Hkv + w.kvh) << shift) + (j & mask);
+  };
+  Quad<T> kq[kKN], vq[kVN];
+  // A unit that lies in one page and is seen whole: its page was looked up a step ahead, its addresses differ by constants.
+  const bool one_page = p.page_size >= kU;
+  auto look = [&](int u) { return u < u1 && one_page ? entries[(kt.walk(u) * kU) >> shift] : 0; };
+  auto whole = [&](int j0) { return one_page && j0 + kU <= n && (n - 1 - j0 < win || j0 + kU <= p.n_sink); };
+  auto load = [&](auto& buf, const T* pool, int u, int entry, auto dim) {
+    constexpr int D = decltype(dim)::value, L = D / 4, TK = 32 / L, N = kU / TK > 0 ? kU / TK : 1;
+    const int j0 = u < u1 ? kt.walk(u) * kU : 0, col = 4 * (lane % L);
+    if (u < u1 && whole(j0)) {
+      const bool there = entry >= 0 && entry < p.num_pages;
+      bad |= !there;
+      const T* at = pool + ((((size_t)entry * p.Hkv + w.kvh) << shift) + (j0 & mask) + lane / L) * D + col;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 q = *reinterpret_cast<const float4*>(q_s + (2 * warp + i) * DK + c);
-        s[i] = fmaf(k.w, q.w, fmaf(k.z, q.z, fmaf(k.y, q.y, fmaf(k.x, q.x, s[i]))));
+      for (int i = 0; i < N; ++i) {
+        if (there && i * TK + lane / L < kU) buf[i].load(at + i * TK * D);
+        else buf[i].zero();
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = i * TK + lane / L;
+      const long long at = u < u1 && t < kU ? place(j0 + t) : -1;
+      if (at >= 0) buf[i].load(pool + at * D + col);
+      else buf[i].zero();
+    }
+  };
+  auto load_k = [&](int u, int entry) { load(kq, kp, u, entry, std::integral_constant<int, DK>()); };
+  auto load_v = [&](int u, int entry) { load(vq, vp, u, entry, std::integral_constant<int, DV>()); };
+
+  int entry = look(u0), next = look(u0 + kWarps);
+  load_k(u0, entry);
+  float4 q[kHB];
+#pragma unroll
+  for (int h = 0; h < kHB; ++h) {
+    Quad<T> x;
+    x.zero();
+    if (h < w.nh) x.load(static_cast<const T*>(p.q) + ((size_t)w.b * p.H + w.h0 + h) * DK + 4 * (lane % kKL));
+    q[h] = x.get();
+  }
+  const float c = p.scale * kLog2e;
+  float m[kHB], l[kHB];  // base 2; l: this lane's tokens
+  float4 acc[kHB];
+#pragma unroll
+  for (int h = 0; h < kHB; ++h) m[h] = -INFINITY, l[h] = 0.f, acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  for (int u = u0; u < u1; u += kWarps) {
+    load_v(u, entry);
+    float s[kHB];
+    int index = 0;
+#pragma unroll
+    for (int h = 0; h < kHB; ++h) {
+      float x[kKN];
+#pragma unroll
+      for (int i = 0; i < kKN; ++i) {
+        const float4 k = kq[i].get();
+        x[i] = fmaf(k.w, q[h].w, fmaf(k.z, q[h].z, fmaf(k.y, q[h].y, k.x * q[h].x)));
+      }
+      s[h] = fold<kKN, kKL>(x, lane, index) * c;
+    }
+    load_k(u + kWarps, next);
+    entry = next, next = look(u + 2 * kWarps);
+    const int t = index * kKT + lane / kKL, j = kt.walk(u) * kU + t;  // this lane's token (shared by lanes of a fold)
+    const bool seen = t < kU && j < n && window::visible(n - 1, j, win, p.n_sink);
+    bool grown = false;
+#pragma unroll
+    for (int h = 0; h < kHB; ++h) {
+      if (!seen) s[h] = -INFINITY;
+      grown |= s[h] > m[h] + kSlack || (m[h] == -INFINITY && s[h] > -INFINITY);
+    }
+    if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+      for (int h = 0; h < kHB; ++h) {
+        float top = s[h];
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, m[h]);
+        const float keep = m[h] == -INFINITY ? 0.f : exp2_fast(m[h] - top);
+        l[h] *= keep;
+        acc[h].x *= keep, acc[h].y *= keep, acc[h].z *= keep, acc[h].w *= keep;
+        m[h] = top;
       }
     }
-    const int j = j0 + lane;
-    const bool vis = j < n && window::visible(n - 1, j, win, p.n_sink);
+    // lanes that share a token write it once
+    const bool mine = (lane & (kKN >= kKL ? 0 : kKL / kKN - 1)) == 0;
+    float e[kHB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!vis) s[i] = -INFINITY;
-      float top = fmaxf(m[i], s[i]);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float base = top == -INFINITY ? 0.f : top;
-      const float keep = expf(m[i] - base), e = expf(s[i] - base);
-      l[i] = l[i] * keep + warp_sum(e);
-      m[i] = top;
-      p_s[lane * kHB + 2 * warp + i] = e;
-      if (lane == 0) keep_s[2 * warp + i] = keep;
+    for (int h = 0; h < kHB; ++h) {
+      e[h] = seen ? exp2_fast(s[h] - m[h]) : 0.f;
+      if (mine) l[h] += e[h];
     }
-    __syncthreads();
+    __syncwarp();
+    if (mine) {
 #pragma unroll
-    for (int h = 0; h < kHB; ++h) acc[h] *= keep_s[h];
-#pragma unroll 8
-    for (int t = tg; t < kTok; t += kGroups) {
-      const float v = v_s[t * (DV + 4) + col];
-      const float4 a = *reinterpret_cast<const float4*>(p_s + t * kHB), b = *reinterpret_cast<const float4*>(p_s + t * kHB + 4);
-      acc[0] = fmaf(a.x, v, acc[0]), acc[1] = fmaf(a.y, v, acc[1]), acc[2] = fmaf(a.z, v, acc[2]), acc[3] = fmaf(a.w, v, acc[3]);
-      acc[4] = fmaf(b.x, v, acc[4]), acc[5] = fmaf(b.y, v, acc[5]), acc[6] = fmaf(b.z, v, acc[6]), acc[7] = fmaf(b.w, v, acc[7]);
+      for (int h = 0; h < kHB; h += 2) *reinterpret_cast<float2*>(&p_s[warp][t][h]) = make_float2(e[h], e[h + 1]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kVN; ++i) {
+      const int tv = i * kVT + lane / kVL;
+      const float4 v = vq[i].get();
+      float pw[kHB];
+      if constexpr (kHB >= 4) {
+#pragma unroll
+        for (int h = 0; h < kHB; h += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(&p_s[warp][tv][h]);
+          pw[h] = a.x, pw[h + 1] = a.y, pw[h + 2] = a.z, pw[h + 3] = a.w;
+        }
+      } else {
+        const float2 a = *reinterpret_cast<const float2*>(&p_s[warp][tv][0]);
+        pw[0] = a.x, pw[1] = a.y;
+      }
+#pragma unroll
+      for (int h = 0; h < kHB; ++h) {
+        acc[h].x = fmaf(pw[h], v.x, acc[h].x), acc[h].y = fmaf(pw[h], v.y, acc[h].y);
+        acc[h].z = fmaf(pw[h], v.z, acc[h].z), acc[h].w = fmaf(pw[h], v.w, acc[h].w);
+      }
     }
   }
   bad = __syncthreads_or(bad);
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) m_s[2 * warp + i] = m[i], l_s[2 * warp + i] = bad ? NAN : l[i];
-  if constexpr (kGroups > 1) {  // the token groups' sums, in their order
-    float* red = k_s;
-    static_assert(4 * kThr <= kTok * (DK + 4), "room for four heads' sums");
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {  // four heads at a time
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 4; ++h) red[h * kThr + tid] = acc[4 * half + h];
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        float x = 0.f;
-        for (int g = 0; g < kGroups; ++g) x += red[h * kThr + g * DV + col];
-        acc[4 * half + h] = x;
-      }
-    }
-  }
-  __syncthreads();
-  if (tg != 0) return;
 #pragma unroll
   for (int h = 0; h < kHB; ++h) {
-    if (h >= w.nh) break;
+    l[h] = warp_sum(l[h]);
+    float4 x = acc[h];
+#pragma unroll
+    for (int o = kVL; o < 32; o <<= 1) {  // the lane groups that read other tokens
+      x.x += __shfl_xor_sync(0xffffffffu, x.x, o), x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+      x.z += __shfl_xor_sync(0xffffffffu, x.z, o), x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+    }
+    if (lane < kVL) *reinterpret_cast<float4*>(&o_s[warp][h][4 * lane]) = x;
+    if (lane == 0) m_s[warp][h] = m[h], l_s[warp][h] = bad ? NAN : l[h];
+  }
+  __syncthreads();
+  for (int e = tid; e < w.nh * DV; e += kThr) {
+    const int h = e / DV, col = e % DV;
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, m_s[i][h]);
+    const float base = M == -INFINITY ? 0.f : M;
+    float sum = 0.f, x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const float f = exp2_fast(m_s[i][h] - base);
+      sum = fmaf(f, l_s[i][h], sum);
+      x = fmaf(f, o_s[i][h][col], x);
+    }
     const size_t head = (size_t)w.b * p.H + w.h0 + h;
     if (p.splits == 1) {
-      const float x = l_s[h] == 0.f ? 0.f : acc[h] / l_s[h];  // nothing visible: zero
-      store_elem(p.o, head * DV + col, x, p.out_dtype);
-      if (col == 0 && p.lse) p.lse[head] = m_s[h] + logf(l_s[h]);
+      store_elem(p.o, head * DV + col, sum == 0.f ? 0.f : x / sum, p.out_dtype);  // nothing visible: zero
+      if (col == 0 && p.lse) p.lse[head] = M * kLn2 + logf(sum);
     } else {
       const size_t at = part_at(p, w.b, w.h0 + h, w.split);
-      p.part[at * DV + col] = acc[h];
-      if (col == 0) part_max(p, DV)[at] = m_s[h], part_sum(p, DV)[at] = l_s[h];
+      p.part[at * DV + col] = x;
+      if (col == 0) part_max(p, DV)[at] = M * kLn2, part_sum(p, DV)[at] = sum;
     }
   }
 }
@@ -211,12 +338,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int D>
 struct StepSmem {
   static constexpr int kTile = kMT * D * 2;            // 16 tokens of k or of v
@@ -232,7 +353,6 @@ __global__ void __launch_bounds__(32 * kMWarps) paged_step_mma_kernel(PagedStepA
   __shared__ float m_s[kMWarps][kMHB], l_s[kMWarps][kMHB];
   constexpr int kChunks = D / 8;                       // 16-byte words of a row
   constexpr int kRows = 32 / kChunks;                  // rows a warp copies at once
-  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const Part w = which<kMHB>(p);
   if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -502,11 +622,17 @@ cudaError_t join(const PagedStepArgs& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, p);
 }
 
+// Query heads per CTA of the fp32 kernel.
+int head_block(int G, int in_dtype) { return in_dtype == kBF16 || G > 4 ? 8 : G > 2 ? 4 : 2; }
+
 template <int DK, int DV>
 cudaError_t step(const PagedStepArgs& p, cudaStream_t stream) {
-  const int G = p.H / p.Hkv;
-  const long long ctas = (long long)p.n * p.Hkv * ((G + kHB - 1) / kHB) * p.splits;
-  paged_step_kernel<DK, DV><<<(unsigned)ctas, kThr, 0, stream>>>(p);
+  const int G = p.H / p.Hkv, hb = head_block(G, p.in_dtype);
+  const unsigned ctas = (unsigned)((long long)p.n * p.Hkv * ((G + hb - 1) / hb) * p.splits);
+  if (p.in_dtype == kBF16) paged_step_kernel<DK, DV, 8, __nv_bfloat16><<<ctas, kThr, 0, stream>>>(p);
+  else if (hb == 8) paged_step_kernel<DK, DV, 8, float><<<ctas, kThr, 0, stream>>>(p);
+  else if (hb == 4) paged_step_kernel<DK, DV, 4, float><<<ctas, kThr, 0, stream>>>(p);
+  else paged_step_kernel<DK, DV, 2, float><<<ctas, kThr, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   return join<DV>(p, stream);
@@ -544,19 +670,12 @@ cudaError_t for_dim(int d, F f) {
 
 int paged_step_splits(int dk, int dv, int in_dtype, int n, int H, int Hkv, long long most_tokens) {
   const int G = H / Hkv;
-  long long s;
-  if (step_mma_supported(dk, dv, in_dtype)) {
-    // Two CTAs fit an SM.  With few (sequence, k/v head) pairs one wave of equal parts; with many, several waves, so that
-    // sequences of different lengths even out.  A part has at least 128 tokens, or its start-up outweighs it.
-    const long long pairs = (long long)n * Hkv * ((G + kMHB - 1) / kMHB), slots = 2 * 148;
-    s = 2 * pairs <= slots ? slots / pairs : (6 * slots + pairs - 1) / pairs;
-    if (s > most_tokens / 128) s = most_tokens / 128;
-  } else {
-    // enough parts for four CTAs on each of 148 SMs, of at least four tiles each
-    const long long pairs = (long long)n * Hkv * ((G + kHB - 1) / kHB), tiles = (most_tokens + kTok - 1) / kTok;
-    s = (4 * 148 + pairs - 1) / pairs;
-    if (s > tiles / 4) s = tiles / 4;
-  }
+  // Two CTAs fit an SM.  With few (sequence, k/v head) pairs one wave of equal parts; with many, several waves, so that
+  // sequences of different lengths even out.  A part has at least 128 tokens, or its start-up outweighs it.
+  const int hb = step_mma_supported(dk, dv, in_dtype) ? kMHB : head_block(G, in_dtype);
+  const long long pairs = (long long)n * Hkv * ((G + hb - 1) / hb), slots = 2 * 148;
+  long long s = 2 * pairs <= slots ? slots / pairs : (6 * slots + pairs - 1) / pairs;
+  if (s > most_tokens / 128) s = most_tokens / 128;
   if (s > kMaxParts) s = kMaxParts;
   return s < 1 ? 1 : (int)s;
 }
