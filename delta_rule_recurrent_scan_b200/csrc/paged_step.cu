@@ -670,12 +670,18 @@ cudaError_t for_dim(int d, F f) {
 
 int paged_step_splits(int dk, int dv, int in_dtype, int n, int H, int Hkv, long long most_tokens) {
   const int G = H / Hkv;
-  // Two CTAs fit an SM.  With few (sequence, k/v head) pairs one wave of equal parts; with many, several waves, so that
-  // sequences of different lengths even out.  A part has at least 128 tokens, or its start-up outweighs it.
+  // Two CTAs fit an SM.  One wave of parts of at least 128 tokens (below that a part is all start-up); for several
+  // sequences, whose lengths differ, up to six waves of parts of at least 512 tokens, which even out.  Measured, 16
+  // sequences of up to 16000 tokens on 4 heads, fp32: 111 us, one wave 154 us; 32 of up to 2000 on 8 heads, bf16: 40 us
+  // with parts of 512 tokens, 50 us with 285; 64 of up to 8192 on 8 heads: 164 us with six waves, 173 us with three.
   const int hb = step_mma_supported(dk, dv, in_dtype) ? kMHB : head_block(G, in_dtype);
   const long long pairs = (long long)n * Hkv * ((G + hb - 1) / hb), slots = 2 * 148;
-  long long s = 2 * pairs <= slots ? slots / pairs : (6 * slots + pairs - 1) / pairs;
-  if (s > most_tokens / 128) s = most_tokens / 128;
+  const auto least = [](long long a, long long b) { return a < b ? a : b; };
+  long long s = least(slots / pairs, most_tokens / 128);
+  if (n > 1) {
+    const long long waves = least((6 * slots + pairs - 1) / pairs, most_tokens / 512);
+    if (waves > s) s = waves;
+  }
   if (s > kMaxParts) s = kMaxParts;
   return s < 1 ? 1 : (int)s;
 }
