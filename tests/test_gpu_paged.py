@@ -397,3 +397,37 @@ def test_serving_run_next_to_the_recurrent_state(dtype, d):
     assert int(pages.refs.sum()) == sum(-(-n // page) for n in pages.lens.tolist())
     kdn.pages_free(pages, torch.arange(8, dtype=torch.int32, device=DEV))
     assert int(pages.refs.abs().sum()) == 0 and bool((pages.table == -1).all())
+
+
+def test_calls_at_once_on_several_streams():
+    """Prefill, backward, decode and page calls of different layers in flight together, each with workspaces of its
+    own, give what they give alone."""
+    jobs, alone = [], []
+    for i in range(3):
+        g = torch.Generator(device=DEV).manual_seed(30 + i)
+        d = (64, 128, 32)[i]
+        dt = torch.bfloat16 if i < 2 else torch.float32
+        q, k, v, dO = (torch.randn(1, h, 700, d, generator=g, device=DEV).to(dt) for h in (4, 2, 2, 4))
+        kp, vp, table, ln, _ = _cache([900, 3000, 5], 2, d, d, 16, dt, seed=i)
+        qs = torch.randn(3, 4, d, generator=g, device=DEV).to(dt)
+        free = sorted(set(range(kp.shape[0])) - set(table.flatten().tolist()))  # pages that no row reads
+        moves = _i32([[int(table[0, 0]), free[0]], [int(table[1, 0]), free[1]]])
+        jobs.append((q, k, v, dO, kp, vp, table, ln, qs, moves))
+
+    def run(job, stream):
+        q, k, v, dO, kp, vp, table, ln, qs, moves = job
+        o, lse = kdn.window_attn(q, k, v, 100, n_sink=3, stream=stream)
+        grads = kdn.window_attn_backward(q, k, v, o, lse, dO, 100, n_sink=3, stream=stream)
+        step = kdn.paged_attn_step(qs, kp, vp, table, ln, stream=stream)
+        kdn.pages_copy(moves, kp, vp, stream=stream)
+        return [o, lse, *grads.values(), *step]
+
+    for job in jobs:
+        alone.append([x.clone() for x in run(job, None)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        together = [run(job, s) for job, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, together):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
