@@ -13,10 +13,11 @@
 //   weights:  exp, masks, row maxima and sums within the warp; the R x 64 weights go to a piece of shared memory of the
 //             warp's own (no CTA barrier between scores and products);
 //   products: acc[R][d / 32] += weight x tile row, again with the weights as broadcast reads.
-// R is 8, or 4 where 8 would leave SMs without a CTA.  Measured (fp32, 3 padded sequences of 1531, 8 heads of 64, window
-// 257, 16 sinks): forward 117 us, backward 384 us; the fp32 pipe is 37 % busy where a CTA runs, the rest waits for
-// shared-memory reads.  4 x 4 values per thread with the rows spread over the lanes (four wavefronts a read): 121 and
-// 615 us; R = 16 (one CTA per SM, longer tail): 163 and 404 us; three CTAs per SM (spills): 146 and 464 us.
+// R is 8, or 4 where 8 would leave SMs without a CTA.  The next tiles are copied (cp.async) while these are used, where a
+// second set of them costs no CTA on the SM.  Measured (fp32, 3 padded sequences of 1531, 8 heads of 64, window 257, 16
+// sinks): forward 108 us, backward 359 us; with one set of tiles 117 and 392 us; 4 x 4 values per thread with the rows
+// spread over the lanes (four wavefronts a read): 121 and 615 us; R = 16 (one CTA per SM, longer tail): 163 and 404 us;
+// three CTAs per SM (spills): 146 and 464 us.  Bound by latency: 8 to 16 warps an SM, the fp32 pipe about 40 % busy.
 //
 // Rows past the sequence's end are staged as zeros, whatever memory holds.
 #include <cmath>
@@ -57,6 +58,44 @@ __device__ __forceinline__ void stage(float* dst, const void* src, size_t row0, 
     *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = x;
   }
 }
+
+// The same, begun: fp32 rows are copied asynchronously (zeros where there is no row), bf16 rows converted at once.  The
+// caller commits, waits and synchronises.
+template <int D, int ROWS>
+__device__ __forceinline__ void begin_stage(float* dst, const void* src, size_t row0, int t0, int len, int dtype) {
+  if (dtype == kBF16) {
+    stage<D, ROWS>(dst, src, row0, t0, len, dtype);
+    return;
+  }
+  constexpr int Q = D / 4;
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  const float* from = static_cast<const float*>(src) + (row0 + t0) * D;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < ROWS * Q; e += kThreads) {
+    const int r = e / Q, c = 4 * (e % Q);
+    const bool there = t0 + r < len;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (r * (D + 4) + c) * 4),
+                 "l"(there ? from + (size_t)r * D + c : static_cast<const float*>(src)), "r"(there ? 16 : 0) : "memory");
+  }
+}
+
+// Shared memory of a CTA beside ``rest`` floats: one set of the two walked tiles, or two, the next tiles being copied while
+// these are used.  With R = 4 (few CTAs) always two, else where they cost no CTA on the SM.
+template <int DK, int DV>
+constexpr int kWalked = kT * (DK + DV + 8);
+constexpr int ctas_per_sm(int floats) { return 227 * 1024 / (floats * 4 + 1024) < 2 ? 227 * 1024 / (floats * 4 + 1024) : 2; }
+template <int DK, int DV, int R>
+constexpr bool two_sets(int rest) {
+  return ctas_per_sm(rest + 2 * kWalked<DK, DV>) >= (R == 4 ? 1 : ctas_per_sm(rest + kWalked<DK, DV>));
+}
+template <int DK, int DV, int R>
+constexpr int total(int rest) { return rest + (two_sets<DK, DV, R>(rest) ? 2 : 1) * kWalked<DK, DV>; }
+template <int DK, int DV, int R>
+constexpr int kFwdRest = kWarps * R * (DK + 4 + kLP);
+template <int DK, int DV, int R>
+constexpr int kDqRest = kWarps * R * (DK + DV + 8 + kLP);
+template <int DK, int DV, int R>
+constexpr int kKeysRest = kWarps * R * (DK + DV + 8 + 2 * kLP);
 
 // s[i][c] = rows[i] . tile[lane + 32 c]
 template <int D, int R>
@@ -176,13 +215,14 @@ __device__ __forceinline__ Where where(unsigned x, int tiles, int heads) {
 }
 
 template <int DK, int DV, int R>
-__global__ void __launch_bounds__(kThreads) window_fwd_kernel(WindowArgs p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kFwdRest<DK, DV, R>)))
+    window_fwd_kernel(WindowArgs p) {
   constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
+  constexpr bool kTwo = two_sets<DK, DV, R>(kFwdRest<DK, DV, R>);
   float* q_s = sm;
-  float* k_s = q_s + kRows * (DK + 4);
-  float* v_s = k_s + kT * (DK + 4);
-  float* p_s = v_s + kT * (DV + 4);
+  float* p_s = q_s + kRows * (DK + 4);
+  float* walked = p_s + kRows * kLP;  // k, then v; the second set behind them
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Where w = where(blockIdx.x, (p.L + kRows - 1) / kRows, p.H);
   const int len = window::seq_len(p, w.b), t0 = w.tile * kRows;
@@ -202,12 +242,21 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WindowArgs p) {
   float m[R], l[R], acc[R][kVals<DV>] = {};  // m in base 2; l: this lane's part of the sum
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.f;
-  for (int it = 0; it < kt.count(); ++it) {
+  const int n = kt.count();
+  auto begin = [&](int it) {
+    float* to = walked + (kTwo ? it & 1 : 0) * kWalked<DK, DV>;
+    begin_stage<DK, kT>(to, p.k, krow, kt.walk(it) * kT, len, p.in_dtype);
+    begin_stage<DV, kT>(to + kT * (DK + 4), p.v, krow, kt.walk(it) * kT, len, p.in_dtype);
+    async_commit();
+  };
+  begin(0);
+  for (int it = 0; it < n; ++it) {
     const int j0 = kt.walk(it) * kT;
-    __syncthreads();  // the previous tile has been read
-    stage<DK, kT>(k_s, p.k, krow, j0, len, p.in_dtype);
-    stage<DV, kT>(v_s, p.v, krow, j0, len, p.in_dtype);
-    __syncthreads();
+    const float* k_s = walked + (kTwo ? it & 1 : 0) * kWalked<DK, DV>;
+    const float* v_s = k_s + kT * (DK + 4);
+    async_wait<0>();
+    __syncthreads();  // this tile is here, and the one before it has been read
+    if (kTwo && it + 1 < n) begin(it + 1);
     float s[R][2], top[R];
     scores<DK, R>(s, q_s + warp * R * (DK + 4), k_s, lane);
     const bool all = j0 + kT - 1 <= t_w && (t_w + R - 1 - j0 < p.window || j0 + kT <= p.n_sink);
@@ -233,6 +282,10 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WindowArgs p) {
     }
     __syncwarp();
     products<DV, R>(acc, w_s, v_s, lane);
+    if (!kTwo && it + 1 < n) {
+      __syncthreads();
+      begin(it + 1);
+    }
   }
   reduce_rows<1>(l);
 #pragma unroll
@@ -261,14 +314,15 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WindowArgs p, int dv)
 
 // A first sweep may make delta = sum P dP, also for the keys' pass (window::exact_delta).
 template <int DK, int DV, int R>
-__global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kDqRest<DK, DV, R>)))
+    window_dq_kernel(WindowArgs p) {
   constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
+  constexpr bool kTwo = two_sets<DK, DV, R>(kDqRest<DK, DV, R>);
   float* q_s = sm;
   float* do_s = q_s + kRows * (DK + 4);
-  float* k_s = do_s + kRows * (DV + 4);
-  float* v_s = k_s + kT * (DK + 4);
-  float* ds_s = v_s + kT * (DV + 4);
+  float* ds_s = do_s + kRows * (DV + 4);
+  float* walked = ds_s + kRows * kLP;  // k, then v; the second set behind them
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Where w = where(blockIdx.x, (p.L + kRows - 1) / kRows, p.H);
   const int len = window::seq_len(p, w.b), t0 = w.tile * kRows;
@@ -293,8 +347,18 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
   float sum[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) sum[i] = 0.f;
+  auto begin = [&](int it) {
+    float* to = walked + (kTwo ? it & 1 : 0) * kWalked<DK, DV>;
+    const int j0 = kt.walk(it < 0 ? it + n : it) * kT;
+    begin_stage<DK, kT>(to, p.k, krow, j0, len, p.in_dtype);
+    begin_stage<DV, kT>(to + kT * (DK + 4), p.v, krow, j0, len, p.in_dtype);
+    async_commit();
+  };
+  begin(-before);
   for (int it = -before; it < n; ++it) {
     const int j0 = kt.walk(it < 0 ? it + n : it) * kT;
+    const float* k_s = walked + (kTwo ? it & 1 : 0) * kWalked<DK, DV>;
+    const float* v_s = k_s + kT * (DK + 4);
     if (it == 0 && before > 0) {
       reduce_rows<1>(sum);
 #pragma unroll
@@ -303,10 +367,9 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
         if (lane == 0 && t_w + i < len) p.delta[qrow + t_w + i] = sum[i];
       }
     }
-    __syncthreads();
-    stage<DK, kT>(k_s, p.k, krow, j0, len, p.in_dtype);
-    stage<DV, kT>(v_s, p.v, krow, j0, len, p.in_dtype);
-    __syncthreads();
+    async_wait<0>();
+    __syncthreads();  // this tile is here, and the one before it has been read
+    if (kTwo && it + 1 < n) begin(it + 1);
     float s[R][2], dp[R][2];
     scores<DK, R>(s, q_s + warp * R * (DK + 4), k_s, lane);
     scores<DV, R>(dp, do_s + warp * R * (DV + 4), v_s, lane);
@@ -322,10 +385,15 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
         else
           w_s[i * kLP + lane + 32 * u] = seen ? P * (dp[i][u] - delta[i]) : 0.f;
       }
-    if (it < 0) continue;
-    __syncwarp();
-    products<DK, R>(acc, w_s, k_s, lane);
-    __syncwarp();
+    if (it >= 0) {
+      __syncwarp();
+      products<DK, R>(acc, w_s, k_s, lane);
+      __syncwarp();
+    }
+    if (!kTwo && it + 1 < n) {
+      __syncthreads();
+      begin(it + 1);
+    }
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -337,15 +405,16 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WindowArgs p) {
 // The keys' pass: every query tile that sees the CTA's keys, of every head that shares them, in a fixed order, so the sums
 // of a gradient are the same on every run.  Key tiles with sinks may be cut (window::key_pass).
 template <int DK, int DV, int R>
-__global__ void __launch_bounds__(kThreads) window_dkdv_kernel(WindowArgs p, KeyPass kp) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kKeysRest<DK, DV, R>)))
+    window_dkdv_kernel(WindowArgs p, KeyPass kp) {
   constexpr int kRows = kWarps * R;
   extern __shared__ __align__(16) float sm[];
+  constexpr bool kTwo = two_sets<DK, DV, R>(kKeysRest<DK, DV, R>);
   float* k_s = sm;
   float* v_s = k_s + kRows * (DK + 4);
-  float* q_s = v_s + kRows * (DV + 4);
-  float* do_s = q_s + kT * (DK + 4);
-  float* p_s = do_s + kT * (DV + 4);
+  float* p_s = v_s + kRows * (DV + 4);
   float* ds_s = p_s + kRows * kLP;
+  float* walked = ds_s + kRows * kLP;  // q, then dO; the second set behind them
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int part;
   const bool is_cut = window::key_tile_of(kp, p.B * p.Hkv, (p.L + kRows - 1) / kRows, blockIdx.x, part);
@@ -370,20 +439,30 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_kernel(WindowArgs p, Key
   float* pw_s = p_s + warp * R * kLP;
   float* dw_s = ds_s + warp * R * kLP;
   float dk[R][kVals<DK>] = {}, dv[R][kVals<DV>] = {};
-  for (int item = first; item < last; ++item) {
+  float lse_next[2], delta_next[2];  // of this lane's queries; behind the end every weight is zero
+  auto begin = [&](int item) {
+    float* to = walked + (kTwo ? item & 1 : 0) * kWalked<DK, DV>;
     const int t0 = (lo + item % per) * kT;
     const size_t qrow = ((size_t)b * p.H + h * G + item / per) * p.L;
-    __syncthreads();
-    stage<DK, kT>(q_s, p.q, qrow, t0, len, p.in_dtype);
-    stage<DV, kT>(do_s, p.dO, qrow, t0, len, p.out_dtype);
-    float lse[2], delta[2];  // of this lane's queries; behind the end every weight is zero
+    begin_stage<DK, kT>(to, p.q, qrow, t0, len, p.in_dtype);
+    begin_stage<DV, kT>(to + kT * (DK + 4), p.dO, qrow, t0, len, p.out_dtype);
+    async_commit();
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int t = t0 + lane + 32 * n;
-      lse[n] = t < len ? p.lse[qrow + t] * kLog2e : INFINITY;
-      delta[n] = t < len ? p.delta[qrow + t] : 0.f;
+    for (int u = 0; u < 2; ++u) {
+      const int t = t0 + lane + 32 * u;
+      lse_next[u] = t < len ? p.lse[qrow + t] * kLog2e : INFINITY;
+      delta_next[u] = t < len ? p.delta[qrow + t] : 0.f;
     }
-    __syncthreads();
+  };
+  if (first < last) begin(first);
+  for (int item = first; item < last; ++item) {
+    const int t0 = (lo + item % per) * kT;
+    const float* q_s = walked + (kTwo ? item & 1 : 0) * kWalked<DK, DV>;
+    const float* do_s = q_s + kT * (DK + 4);
+    const float lse[2] = {lse_next[0], lse_next[1]}, delta[2] = {delta_next[0], delta_next[1]};
+    async_wait<0>();
+    __syncthreads();  // these tiles are here, and the ones before them have been read
+    if (kTwo && item + 1 < last) begin(item + 1);
     float s[R][2], dp[R][2];
     scores<DK, R>(s, k_s + warp * R * (DK + 4), q_s, lane);
     scores<DV, R>(dp, v_s + warp * R * (DV + 4), do_s, lane);
@@ -401,6 +480,10 @@ __global__ void __launch_bounds__(kThreads) window_dkdv_kernel(WindowArgs p, Key
     products<DV, R>(dv, pw_s, do_s, lane);
     products<DK, R>(dk, dw_s, q_s, lane);
     __syncwarp();
+    if (!kTwo && item + 1 < last) {
+      __syncthreads();
+      begin(item + 1);
+    }
   }
   if (is_cut) {  // [tile][part][dk, then dv] of the CTA's rows, fp32
     float* out = kp.part + (((size_t)kp.head * kp.sinks + tile) * kp.parts + part) * kRows * (DK + DV);
@@ -453,13 +536,13 @@ long long row_tiles(const WindowArgs& p, int rows, int heads) { return (long lon
 template <int DK, int DV, int R>
 cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
   constexpr int kRows = kWarps * R;
-  return run(window_fwd_kernel<DK, DV, R>, kRows * (DK + 4 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
+  return run(window_fwd_kernel<DK, DV, R>, total<DK, DV, R>(kFwdRest<DK, DV, R>), row_tiles(p, kRows, p.H), stream, p);
 }
 
 template <int DK, int DV, int R>
 cudaError_t dq_pass(const WindowArgs& p, cudaStream_t stream) {
   constexpr int kRows = kWarps * R;
-  return run(window_dq_kernel<DK, DV, R>, kRows * (DK + DV + 8 + kLP) + kT * (DK + DV + 8), row_tiles(p, kRows, p.H), stream, p);
+  return run(window_dq_kernel<DK, DV, R>, total<DK, DV, R>(kDqRest<DK, DV, R>), row_tiles(p, kRows, p.H), stream, p);
 }
 
 // Keys per CTA of the keys' pass, in units of the warps: 4 where 8 would leave SMs without a CTA.
@@ -485,7 +568,7 @@ cudaError_t keys_pass(const WindowArgs& p, cudaStream_t stream) {
   KeyPass kp = cut<R>(p.B, p.H, p.Hkv, p.L, p.window, p.n_sink);
   kp.part = static_cast<float*>(p.scratch) + ((size_t)p.B * p.H * p.L + 63) / 64 * 64;  // behind delta
   const long long ctas = (long long)p.B * p.Hkv * kp.sinks * (kp.parts - 1) + row_tiles(p, kRows, p.Hkv);
-  const cudaError_t e = run(window_dkdv_kernel<DK, DV, R>, kRows * (DK + DV + 8 + 2 * kLP) + kT * (DK + DV + 8), ctas, stream, p, kp);
+  const cudaError_t e = run(window_dkdv_kernel<DK, DV, R>, total<DK, DV, R>(kKeysRest<DK, DV, R>), ctas, stream, p, kp);
   if (e != cudaSuccess || kp.sinks == 0) return e;
   const size_t values = (size_t)p.B * p.Hkv * kp.sinks * kRows * (DK + DV);
   window_sum_parts_kernel<<<(unsigned)((values + 255) / 256), 256, 0, stream>>>(p, kp, kRows, DK, DV);
