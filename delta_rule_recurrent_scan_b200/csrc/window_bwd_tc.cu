@@ -14,8 +14,8 @@
 //            tile's S and dP (two buffers) run while this tile's dS is made.
 //
 // P and dS are rounded to bf16 for their product (the other operand's type; 2^-8 of a weight at most); the sums are fp32.
-// A warpgroup takes half of a tile's columns: thread = (lane, half).  One load warp (TMA rings of two slots), one warp
-// whose first lane issues the products.  Rows behind a sequence's end are zeroed in shared memory.
+// A warpgroup takes half of a tile's columns: thread = (lane, half).  One load warp (TMA rings), one warp whose first
+// lane issues the products.  Rows behind a sequence's end are zeroed in shared memory.
 //
 // Key tiles with sinks may be cut into parts (window::key_pass); part: [B, Hkv, sinks, parts, 2, 128, D].
 #include "window_tc.cuh"
@@ -30,9 +30,14 @@ template <int D>
 struct Smem {
   static constexpr int kTile = (D / 64) * kPanel;
   static constexpr int kFixed = 0;                 // the two tiles a CTA keeps
-  static constexpr int kRing = 2 * kTile;          // two slots of the two tiles it walks
-  static constexpr int kTotal = 6 * kTile;
+  static constexpr int kLong = 2 * kTile;          // the walked tiles of two products, kSlots of them
+  static constexpr int kShort = 5 * kTile;         // the other walked tiles, two of them
+  static constexpr int kTotal = 7 * kTile;
 };
+// A tile that two products use (q in the keys' pass, k in the queries') leaves its slot only with the second, just before
+// the tile two steps on is wanted: with two slots every step waited about 1500 cycles for that copy.  A third one: 2
+// sequences of 4096, 16 heads on 4, d 128, window 1024, backward 298 -> 271 us; one of 8192 without a window 1146 -> 1004.
+constexpr unsigned kSlots = 3;
 
 // ------------------------------------------------------------------------------------------ per-query scalars
 // rows[token] = (-lse log2(e), -delta), and dO as bf16 where it came as fp32.  D / 8 lanes per token.
@@ -79,6 +84,11 @@ __global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* 
 }
 
 // ------------------------------------------------------------------------------------------ dk, dv
+struct DkdvState {          // behind the tiles in shared memory: with them it fills the 227 KB of a block
+  float rows[2][2][kT];     // -lse log2(e), -delta
+  uint64_t kv_full, q_full[kSlots], q_empty[kSlots], do_full[2], do_empty[2], rows_full[2], s_ready, p_ready, dp_ready, ds_ready, done;
+  uint32_t tmem_base;
+};
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     window_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -86,11 +96,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                           const float2* rows, KeyPass kp) {
   using S = Smem<D>;
   constexpr int kNP = D / 64;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(16) float rows_s[2][2][kT];  // -lse log2(e), -delta
-  __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], s_ready, p_ready, dp_ready, ds_ready, done;
-  __shared__ uint32_t tmem_base;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  DkdvState& st = *reinterpret_cast<DkdvState*>(sm + S::kTotal);
+  auto& rows_s = st.rows;
+  uint64_t &kv_full = st.kv_full, &s_ready = st.s_ready, &p_ready = st.p_ready, &dp_ready = st.dp_ready, &ds_ready = st.ds_ready,
+           &done = st.done;
+  uint64_t *q_full = st.q_full, *q_empty = st.q_empty, *do_full = st.do_full, *do_empty = st.do_empty, *rows_full = st.rows_full;
+  if (sm100::smem_u32(sm) & 1023) {  // never seen; the tiles' layout wants it and there is no room to align them here
+    raise_status(p.status, kStatusTimeout);
+    return;
+  }
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
@@ -112,23 +127,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (tid == 0) {
     sm100::mbar_init(&kv_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&q_full[i], 33), sm100::mbar_init(&q_empty[i], 1);  // the copy and 32 lanes' row scalars
-      sm100::mbar_init(&do_full[i], 1), sm100::mbar_init(&do_empty[i], 1);
-    }
+    for (int i = 0; i < (int)kSlots; ++i) sm100::mbar_init(&q_full[i], 1), sm100::mbar_init(&q_empty[i], 1);
+    for (int i = 0; i < 2; ++i)
+      sm100::mbar_init(&do_full[i], 1), sm100::mbar_init(&do_empty[i], 1), sm100::mbar_init(&rows_full[i], 1);
     sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&p_ready, 8);
     sm100::mbar_init(&dp_ready, 1), sm100::mbar_init(&ds_ready, 8);
     sm100::mbar_init(&done, 1);
     sm100::fence_mbar_init();
   }
   if (warp == 9) {
-    sm100::tmem_alloc(&tmem_base, 512);
+    sm100::tmem_alloc(&st.tmem_base, 512);
     sm100::tmem_relinquish();
   }
   sm100::tc_fence_before();
   __syncthreads();
   sm100::tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = st.tmem_base;
   const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
   bool fine = true;
 
@@ -141,53 +155,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       load_tile<kNP>(sm + S::kFixed + S::kTile, &tm_v, &kv_full, j0, b * p.Hkv + kvh);
     }
     int it = 0;
-    bool q_sent = false;
+    bool q_sent = false, do_sent = false;
     for (; it < n; ++it) {
-      const int slot = it & 1, round = it >> 1, item = first + it;
+      const int slot = it & 1, round = it >> 1, qslot = it % kSlots, qround = it / kSlots, item = first + it;
       const int row = b * p.H + kvh * G + item / per, t0 = (lo + item % per) * kT;
-      q_sent = false;
-      if (round > 0) fine = warp_wait(&q_empty[slot], (round - 1) & 1);
+      q_sent = do_sent = false;
+      if (qround > 0) fine = warp_wait(&q_empty[qslot], (qround - 1) & 1);
       if (!fine) break;
       if (lane == 0) {
-        sm100::mbar_arrive_expect_tx(&q_full[slot], S::kTile);
-        load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_q, &q_full[slot], t0, row);
+        sm100::mbar_arrive_expect_tx(&q_full[qslot], S::kTile);
+        load_tile<kNP>(sm + S::kLong + qslot * S::kTile, &tm_q, &q_full[qslot], t0, row);
       }
       q_sent = true;
-      // the rows' scalars; behind the end -lse = -inf makes every weight zero
+      float2 v[kT / 32];  // the rows' scalars; behind the end -lse = -inf makes every weight zero
 #pragma unroll
       for (int u = 0; u < kT / 32; ++u) {
         const int r = lane + 32 * u;
-        const float2 v = t0 + r < len ? rows[(size_t)row * p.L + t0 + r] : make_float2(-INFINITY, 0.f);
-        rows_s[slot][0][r] = v.x, rows_s[slot][1][r] = v.y;
+        v[u] = t0 + r < len ? rows[(size_t)row * p.L + t0 + r] : make_float2(-INFINITY, 0.f);
       }
-      sm100::mbar_arrive(&q_full[slot]);
       if (round > 0) fine = warp_wait(&do_empty[slot], (round - 1) & 1);
       if (!fine) break;
       if (lane == 0) {
         sm100::mbar_arrive_expect_tx(&do_full[slot], S::kTile);
-        load_tile<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, &tm_do, &do_full[slot], t0, row);
+        load_tile<kNP>(sm + S::kShort + slot * S::kTile, &tm_do, &do_full[slot], t0, row);
       }
+      do_sent = true;
+      // dK(it - 2) has ended, and with it every read of that tile's scalars
+      if (it > 1) fine = warp_wait(&q_empty[(it - 2) % kSlots], ((it - 2) / kSlots) & 1);
+      if (!fine) break;
+#pragma unroll
+      for (int u = 0; u < kT / 32; ++u) rows_s[slot][0][lane + 32 * u] = v[u].x, rows_s[slot][1][lane + 32 * u] = v[u].y;
+      warp_arrive(&rows_full[slot]);
     }
     if (!fine) {  // nothing of this CTA may be in flight when it ends
       sm100::mbar_wait_bounded(&kv_full, 0, kWaitCycles);
-      for (int back = it > 1 ? it - 1 : 0; back <= it && back < n; ++back) {
-        if (back < it || q_sent) sm100::mbar_wait_bounded(&q_full[back & 1], (back >> 1) & 1, kWaitCycles);
-        if (back < it) sm100::mbar_wait_bounded(&do_full[back & 1], (back >> 1) & 1, kWaitCycles);
+      for (int back = it > 2 ? it - 2 : 0; back <= it && back < n; ++back) {
+        if (back < it || q_sent) sm100::mbar_wait_bounded(&q_full[back % kSlots], (back / kSlots) & 1, kWaitCycles);
+        if (back < it || do_sent) sm100::mbar_wait_bounded(&do_full[back & 1], (back >> 1) & 1, kWaitCycles);
       }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------------------ products
     const uint32_t k_addr = sm100::smem_u32(sm + S::kFixed), v_addr = k_addr + S::kTile;
-    const uint32_t ring = sm100::smem_u32(sm + S::kRing);
-    auto q_of = [&](int it) { return ring + 2 * (it & 1) * S::kTile; };
-    auto do_of = [&](int it) { return ring + (2 * (it & 1) + 1) * S::kTile; };
+    const uint32_t ring_q = sm100::smem_u32(sm + S::kLong), ring_do = sm100::smem_u32(sm + S::kShort);
+    auto q_of = [&](int it) { return ring_q + it % kSlots * S::kTile; };
+    auto do_of = [&](int it) { return ring_do + (it & 1) * S::kTile; };
     auto end_of = [&](int it) { return len - (lo + (first + it) % per) * kT; };  // rows of this tile inside the sequence
     auto issue_s = [&](int it) {
-      if (end_of(it) < kT) zero_rows<kNP>(sm + S::kRing + 2 * (it & 1) * S::kTile, end_of(it), lane);
+      if (end_of(it) < kT) zero_rows<kNP>(sm + S::kLong + it % kSlots * S::kTile, end_of(it), lane);
       if (lane == 0) mma_rows<D>(t_s, rows_desc(k_addr), rows_desc(q_of(it))), sm100::mma_commit(&s_ready);
     };
     auto issue_dp = [&](int it) {
-      if (end_of(it) < kT) zero_rows<kNP>(sm + S::kRing + (2 * (it & 1) + 1) * S::kTile, end_of(it), lane);
+      if (end_of(it) < kT) zero_rows<kNP>(sm + S::kShort + (it & 1) * S::kTile, end_of(it), lane);
       if (lane == 0) mma_rows<D>(t_dp, rows_desc(v_addr), rows_desc(do_of(it))), sm100::mma_commit(&dp_ready);
     };
     if (n > 0) {
@@ -204,7 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sm100::mma_commit(&do_empty[slot]);
       }
       if (it + 1 < n) {
-        fine = warp_wait(&q_full[next], next_round & 1);
+        fine = warp_wait(&q_full[(it + 1) % kSlots], ((it + 1) / kSlots) & 1);
         if (!fine) break;
         issue_s(it + 1);
       }
@@ -213,7 +232,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::tc_fence_after();
       if (lane == 0) {
         mma_weights<D>(t_dk, t_dp, 64, cols_desc(q_of(it)), it > 0);
-        sm100::mma_commit(&q_empty[slot]);
+        sm100::mma_commit(&q_empty[it % kSlots]);
       }
       if (it + 1 < n) {
         fine = warp_wait(&do_full[next], next_round & 1);
@@ -234,7 +253,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const bool sink = j < p.n_sink;
     for (int it = 0; it < n; ++it) {
       const int t0 = (lo + (first + it) % per) * kT + 64 * half;  // this half's first query
-      fine = warp_wait(&q_full[it & 1], (it >> 1) & 1) && warp_wait(&s_ready, it & 1);  // the row scalars and S^T
+      fine = warp_wait(&rows_full[it & 1], (it >> 1) & 1) && warp_wait(&s_ready, it & 1);  // the row scalars and S^T
       if (!fine) break;
       sm100::tc_fence_after();
       float s[2][32];
@@ -397,15 +416,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kNP = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready[2], done, last;
+  __shared__ uint64_t q_full, q_empty, k_full[kSlots], k_empty[kSlots], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready[2], done, last;
   __shared__ uint32_t tmem_base;
   __shared__ float delta_s[2][kT];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     sm100::mbar_init(&q_full, 1), sm100::mbar_init(&q_empty, 1);
+    for (int i = 0; i < (int)kSlots; ++i) sm100::mbar_init(&k_full[i], 1), sm100::mbar_init(&k_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&k_full[i], 1), sm100::mbar_init(&k_empty[i], 1);
       sm100::mbar_init(&v_full[i], 1), sm100::mbar_init(&v_empty[i], 1);
       sm100::mbar_init(&dp_ready[i], 1), sm100::mbar_init(&ds_ready[i], 8);
     }
@@ -436,17 +455,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int row = w.b * p.Hkv + w.kvh;
         const int steps = w.before + w.n;
         for (int it = 0; it < steps; ++it) {
-          const unsigned slot = nk & 1;
+          const unsigned kslot = nk % kSlots, slot = nv & 1;
           const int j0 = w.kt.walk(it < w.n ? it : it - w.n) * kT;
-          if (nk > 1) fine = sm100::mbar_wait_bounded(&k_empty[slot], ((nk >> 1) - 1) & 1, kWaitCycles);
+          if (nk >= kSlots) fine = sm100::mbar_wait_bounded(&k_empty[kslot], (nk / kSlots - 1) & 1, kWaitCycles);
           if (!fine) break;
-          sm100::mbar_arrive_expect_tx(&k_full[slot], S::kTile);
-          load_tile<kNP>(sm + S::kRing + 2 * slot * S::kTile, &tm_k, &k_full[slot], j0, row);
+          sm100::mbar_arrive_expect_tx(&k_full[kslot], S::kTile);
+          load_tile<kNP>(sm + S::kLong + kslot * S::kTile, &tm_k, &k_full[kslot], j0, row);
           ++nk;
           if (nv > 1) fine = sm100::mbar_wait_bounded(&v_empty[slot], ((nv >> 1) - 1) & 1, kWaitCycles);
           if (!fine) break;
           sm100::mbar_arrive_expect_tx(&v_full[slot], S::kTile);
-          load_tile<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, &tm_v, &v_full[slot], j0, row);
+          load_tile<kNP>(sm + S::kShort + slot * S::kTile, &tm_v, &v_full[slot], j0, row);
           ++nv;
           if (it == 0) {
             if (nq > 0) fine = sm100::mbar_wait_bounded(&q_empty, (nq - 1) & 1, kWaitCycles);
@@ -460,13 +479,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!fine) {  // nothing of this CTA may be in flight when it ends
         if (nq > 0) sm100::mbar_wait_bounded(&q_full, (nq - 1) & 1, kWaitCycles);
-        for (unsigned c = nk > 2 ? nk - 2 : 0; c < nk; ++c) sm100::mbar_wait_bounded(&k_full[c & 1], (c >> 1) & 1, kWaitCycles);
+        for (unsigned c = nk > kSlots ? nk - kSlots : 0; c < nk; ++c) sm100::mbar_wait_bounded(&k_full[c % kSlots], (c / kSlots) & 1, kWaitCycles);
         for (unsigned c = nv > 2 ? nv - 2 : 0; c < nv; ++c) sm100::mbar_wait_bounded(&v_full[c & 1], (c >> 1) & 1, kWaitCycles);
       }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------------------ products
-    const uint32_t ring = sm100::smem_u32(sm + S::kRing);
+    const uint32_t ring_k = sm100::smem_u32(sm + S::kLong), ring_v = sm100::smem_u32(sm + S::kShort);
     const uint64_t q_desc = rows_desc(sm100::smem_u32(sm + S::kFixed)), do_desc = rows_desc(sm100::smem_u32(sm + S::kFixed + S::kTile));
     unsigned c = 0, nq = 0;  // key tiles and works begun
     for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
@@ -478,21 +497,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // S and dP of the it-th step, the c-th of this CTA: S is free once step c - 1 is in registers.  k and v rows behind
       // the end are zeroed (their weights are zero).
       auto issue = [&](int it) {
-        const unsigned slot = c & 1;
-        fine = warp_wait(&k_full[slot], (c >> 1) & 1) && warp_wait(&v_full[slot], (c >> 1) & 1) &&
+        const unsigned kslot = c % kSlots, slot = c & 1;
+        fine = warp_wait(&k_full[kslot], (c / kSlots) & 1) && warp_wait(&v_full[slot], (c >> 1) & 1) &&
                (c == 0 || warp_wait(&s_free, (c - 1) & 1));
         if (!fine) return;
         sm100::tc_fence_after();
         const int inside = w.len - w.kt.walk(it < w.n ? it : it - w.n) * kT;
         if (inside < kT) {
-          zero_rows<kNP>(sm + S::kRing + 2 * slot * S::kTile, inside, lane);
-          zero_rows<kNP>(sm + S::kRing + (2 * slot + 1) * S::kTile, inside, lane);
+          zero_rows<kNP>(sm + S::kLong + kslot * S::kTile, inside, lane);
+          zero_rows<kNP>(sm + S::kShort + slot * S::kTile, inside, lane);
         }
         if (lane == 0) {
-          const uint64_t k_desc = rows_desc(ring + 2 * slot * S::kTile);
-          mma_rows<D>(t_s, q_desc, k_desc);
+          mma_rows<D>(t_s, q_desc, rows_desc(ring_k + kslot * S::kTile));
           sm100::mma_commit(&s_ready);
-          mma_rows<D>(t_dp + 128 * slot, do_desc, k_desc + (S::kTile >> 4));
+          mma_rows<D>(t_dp + 128 * slot, do_desc, rows_desc(ring_v + slot * S::kTile));
           sm100::mma_commit(&dp_ready[slot]);
           sm100::mma_commit(&v_empty[slot]);
           if (it + 1 == steps) sm100::mma_commit(&q_empty);
@@ -503,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ++nq;
       if (fine) issue(0);
       for (int it = 0; it < steps && fine; ++it) {
-        const unsigned mine = c - 1, slot = mine & 1;  // step ``it``
+        const unsigned mine = c - 1, kslot = mine % kSlots, slot = mine & 1;  // step ``it``
         if (it + 1 < steps) issue(it + 1);
         if (!fine) break;
         fine = warp_wait(&ds_ready[slot], (mine >> 1) & 1);
@@ -511,8 +529,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sm100::tc_fence_after();
         if (lane == 0) {
           const int sweep = it - w.before;  // >= 0: the tile of the sweep that adds up dq
-          if (sweep >= 0) mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring + 2 * slot * S::kTile), sweep > 0);
-          sm100::mma_commit(&k_empty[slot]);
+          if (sweep >= 0) mma_weights<D>(t_dq, t_dp + 128 * slot, 64, cols_desc(ring_k + kslot * S::kTile), sweep > 0);
+          sm100::mma_commit(&k_empty[kslot]);
           if (it + 1 == steps) sm100::mma_commit(&done);
         }
       }
@@ -672,11 +690,11 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   window_rows_kernel<D><<<(unsigned)((tokens * (D / 8) + 255) / 256), 256, 0, stream>>>(p, rows, dO16);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int smem = Smem<D>::kTotal + 1024, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
+  const int smem = Smem<D>::kTotal + 1024, key_smem = Smem<D>::kTotal + (int)sizeof(DkdvState), tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return cudaErrorInvalidDevice;
-  e = cudaFuncSetAttribute(window_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(window_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, key_smem);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(window_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -689,7 +707,7 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   window_dq_tc_kernel<D><<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, qp);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, kp);
+  window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, key_smem, stream>>>(tq, tk, tv, td, p, rows, kp);
   e = cudaGetLastError();
   if (e != cudaSuccess || kp.sinks == 0) return e;
   const size_t words = (size_t)bh * kp.sinks * 2 * kT * D / 8;
