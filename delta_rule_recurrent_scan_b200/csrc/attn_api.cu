@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cstdint>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/kdn.h"
@@ -49,6 +51,29 @@ kdn_status check_workspace(const void* ws, size_t bytes, size_t need) {
     return fail(KDN_ERR_INVALID_ARG, "workspace_bytes " + std::to_string(bytes) + " < required " + std::to_string(need));
   return KDN_OK;
 }
+
+// The kernels write parts of an output while others still read the inputs: no output may share memory with an input
+// or with another output.
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+kdn_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x != 0 && y != 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
+  };
+  for (const Span* a = outs.begin(); a != outs.end(); ++a) {
+    for (const Span* b = a + 1; b != outs.end(); ++b)
+      if (meet(*a, *b)) return fail(KDN_ERR_INVALID_ARG, std::string(a->name) + " overlaps " + b->name);
+    for (const Span& b : ins)
+      if (meet(*a, b)) return fail(KDN_ERR_INVALID_ARG, std::string(a->name) + " overlaps " + b.name);
+  }
+  return KDN_OK;
+}
+
+size_t elem_bytes(kdn_dtype t) { return t == KDN_BF16 ? 2 : 4; }
 
 // ---------------------------------------------------------------------------------------- paged cache
 bool pages_sizes_ok(const kdn_pages* p) {
@@ -102,8 +127,6 @@ kdn_status check_pool(int kv_heads, int dk, int dv, kdn_dtype dtype) {
   return KDN_OK;
 }
 
-size_t elem_bytes(kdn_dtype t) { return t == KDN_BF16 ? 2 : 4; }
-
 }  // namespace
 
 extern "C" {
@@ -124,6 +147,11 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
                            size_t workspace_bytes, void* stream) {
   KDN_TRY(window_checks(dims, kv_heads, window, n_sink, scale));
   const bool none = dims->L == 0;
+  const size_t in = elem_bytes(dims->in_dtype), rows = (size_t)dims->B * dims->H * dims->L, keys = rows / dims->H * kv_heads;
+  const Span q_{"q", q, rows * dims->dk * in}, k_{"k", k, keys * dims->dk * in}, v_{"v", v, keys * dims->dv * in};
+  const Span o_{"o", o, rows * dims->dv * elem_bytes(dims->out_dtype)}, lse_{"lse", lse, rows * 4};
+  const Span ws_{"workspace", workspace, workspace_bytes};
+  KDN_TRY(check_apart({o_, lse_, ws_}, {q_, k_, v_}));
   KDN_TRY(check_ptr(q, "q", 16, none));
   KDN_TRY(check_ptr(k, "k", 16, none));
   KDN_TRY(check_ptr(v, "v", 16, none));
@@ -151,6 +179,12 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
                                     size_t workspace_bytes, void* stream) {
   KDN_TRY(window_checks(dims, kv_heads, window, n_sink, scale));
   const bool none = dims->L == 0;
+  const size_t in = elem_bytes(dims->in_dtype), rows = (size_t)dims->B * dims->H * dims->L, keys = rows / dims->H * kv_heads;
+  const Span q_{"q", q, rows * dims->dk * in}, k_{"k", k, keys * dims->dk * in}, v_{"v", v, keys * dims->dv * in};
+  const Span o_{"o", o, rows * dims->dv * elem_bytes(dims->out_dtype)}, lse_{"lse", lse, rows * 4};
+  const Span ws_{"workspace", workspace, workspace_bytes};
+  const Span dO_{"dO", dO, o_.bytes}, dq_{"dq", dq, q_.bytes}, dk_{"dk", dk, k_.bytes}, dv_{"dv", dv, v_.bytes};
+  KDN_TRY(check_apart({dq_, dk_, dv_, ws_}, {q_, k_, v_, o_, lse_, dO_}));
   KDN_TRY(check_ptr(q, "q", 16, none));
   KDN_TRY(check_ptr(k, "k", 16, none));
   KDN_TRY(check_ptr(v, "v", 16, none));
@@ -243,6 +277,7 @@ kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const
                            void* v_pages, void* stream) {
   KDN_TRY(check_pages(pages));
   if (n < 0 || tokens < 0) return fail(KDN_ERR_INVALID_ARG, "n and tokens must be >= 0");
+  if (tokens > 1 << 24) return fail(KDN_ERR_UNSUPPORTED, "tokens must be at most 2^24");
   KDN_TRY(check_pool(kv_heads, dk, dv, dtype));
   const bool none = n == 0 || tokens == 0;
   KDN_TRY(check_ptr(pages->table, "table", 4, false));
@@ -285,6 +320,9 @@ kdn_status kdn_paged_attn_step(const kdn_pages* pages, int n, const int* rows, i
   KDN_TRY(check_window(window, 0, n_sink, scale));
   if ((long long)n * H > (1 << 24)) return fail(KDN_ERR_UNSUPPORTED, "n*H must be at most 2^24");
   if (rows == nullptr && n > pages->rows) return fail(KDN_ERR_INVALID_ARG, "n exceeds the table's rows");
+  const size_t heads = (size_t)n * H, pool = (size_t)pages->num_pages * kv_heads * pages->page_size * elem_bytes(in_dtype);
+  KDN_TRY(check_apart({{"o", o, heads * dv * elem_bytes(out_dtype)}, {"lse", lse, heads * 4}, {"workspace", workspace, workspace_bytes}},
+                      {{"q", q, heads * dk * elem_bytes(in_dtype)}, {"k_pages", k_pages, pool * dk}, {"v_pages", v_pages, pool * dv}}));
   KDN_TRY(check_ptr(pages->table, "table", 4, false));
   KDN_TRY(check_ptr(pages->lens, "lens", 4, false));
   KDN_TRY(check_ptr(rows, "rows", 4, true));

@@ -295,7 +295,8 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * q [B,H,L,d_k], k [B,kv_heads,L,d_k], v [B,kv_heads,L,d_v] (dims->in_dtype): query head h reads k/v head
  * h / (H / kv_heads); kv_heads divides H.  lens [B] int32 or NULL (= L): tokens of each sequence, held to
  * [0, L]; what memory holds behind a sequence's last token takes no part (it may be NaN), and its rows of o
- * and lse are left as they were (zero_rest = 0) or set to zero (1).  window >= 1 (>= L: plain causal attention), n_sink >= 0, 0 < scale <= 1e30.
+ * and lse are left as they were (zero_rest = 0) or set to zero (1).  window >= 1 (>= L: plain causal attention),
+ * n_sink >= 0, 0 < scale <= 1e30.  Here and in the two calls below no output may overlap an input or another output.
  * The sequences' own tokens must be finite: a hidden token's weight is 0, and 0 times its value has to be 0.
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
@@ -313,8 +314,9 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
  * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
  * gradients do not change from run to run.  Where rows see few keys and o is bf16, delta is made from P and dP
- * instead of the rounded o.  Rows behind a sequence's last token are left as they were or set to
- * zero (zero_rest), in all three; lse has no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1) bytes. */
+ * instead of the rounded o.  Rows behind a sequence's last token are left as they were or set to zero (zero_rest),
+ * in all three; lse has no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink,
+ * 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
                                     const void* v, const int* lens, int zero_rest, int window, int n_sink, float scale,
                                     const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
@@ -373,9 +375,9 @@ KDN_EXPORT kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int
                           kdn_dtype dtype, void* k_pages, void* v_pages, void* stream);
 
 /* Writes the newest tokens of rows rows[0..n) into one layer's pages, after kdn_pages_reserve has added them:
- * k_new [n, kv_heads, tokens, d_k], v_new [n, kv_heads, tokens, d_v]; of entry i the first counts[i] (NULL: tokens)
- * are the last counts[i] tokens of the row.  Entries whose row, count or page is out of range are skipped; of a row
- * listed twice either entry may be the one that stays. */
+ * k_new [n, kv_heads, tokens, d_k], v_new [n, kv_heads, tokens, d_v]; of entry i the first counts[i] (NULL: tokens,
+ * at most 2^24) are the last counts[i] tokens of the row.  Entries whose row, count or page is out of range are
+ * skipped; of a row listed twice either entry may be the one that stays. */
 KDN_EXPORT kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens,
                            int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new,
                            void* k_pages, void* v_pages, void* stream);

@@ -115,6 +115,53 @@ def test_paged_cache_refusals(L):
     assert L.kdn_status_string(6).decode() == "KDN_ERR_CAPACITY"
 
 
+def test_outputs_may_not_overlap(L):
+    """Refused from the addresses alone, before anything reads them."""
+    d = kdn.Dims(1, 4, 8, 64, 64, 0, 1, 1, 0)  # bf16: q, o 4096 bytes, k, v (2 heads) 2048, lse 128
+    at = dict(q=0x10000, k=0x20000, v=0x30000, o=0x40000, lse=0x50000, dO=0x60000, dq=0x70000, dk=0x80000, dv=0x90000,
+              ws=0xa0000)
+
+    def forward(**new):
+        a = {**at, **new}
+        st = L.kdn_window_attn(ctypes.byref(d), 2, a["q"], a["k"], a["v"], None, 0, 4, 0, 1.0, a["o"], a["lse"], a["ws"], 256, None)
+        return st, L.kdn_last_error()
+
+    def backward(**new):
+        a = {**at, **new}
+        st = L.kdn_window_attn_backward(ctypes.byref(d), 2, a["q"], a["k"], a["v"], None, 0, 4, 0, 1.0, a["o"], a["lse"],
+                                        a["dO"], a["dq"], a["dk"], a["dv"], a["ws"], 256, None)
+        return st, L.kdn_last_error()
+
+    c = kdn.PagesC(num_pages=8, page_size=16, rows=4, max_pages=2)
+
+    def step(**new):
+        a = {**at, **new}  # q, o [2, 4, 64], pages [8, 2, 16, 64]: 32,768 bytes
+        st = L.kdn_paged_attn_step(ctypes.byref(c), 2, None, 4, 2, 64, 64, 1, 1, a["q"], a["k"], a["v"], 0, 0, 1.0, a["o"],
+                                   a["lse"], a["ws"], 256, None)
+        return st, L.kdn_last_error()
+
+    for call, new, says in (
+            (forward, dict(o=at["q"]), b"o overlaps q"), (forward, dict(o=at["k"] + 2032), b"o overlaps k"),
+            (forward, dict(o=at["v"] - 4080), b"o overlaps v"), (forward, dict(lse=at["o"] + 4080), b"o overlaps lse"),
+            (forward, dict(lse=at["q"] - 112), b"lse overlaps q"), (forward, dict(ws=at["v"]), b"workspace overlaps v"),
+            (backward, dict(dq=at["dO"]), b"dq overlaps dO"), (backward, dict(dk=at["k"]), b"dk overlaps k"),
+            (backward, dict(dv=at["dk"] + 2032), b"dk overlaps dv"), (backward, dict(dq=at["lse"]), b"dq overlaps lse"),
+            (backward, dict(dv=at["o"] + 4080), b"dv overlaps o"),
+            (step, dict(o=at["q"] + 1008), b"o overlaps q"), (step, dict(lse=at["k"] + 32752), b"lse overlaps k_pages"),
+            (step, dict(ws=at["v"] + 256), b"workspace overlaps v_pages")):
+        st, said = call(**new)
+        assert st == kdn.KDN_ERR_INVALID_ARG and said.endswith(says), (says, said)
+    for call, new in ((forward, dict(o=at["q"] + 4096)), (backward, dict(dq=at["dO"] + 4096)),
+                      (backward, dict(dv=at["dk"] + 2048)), (step, dict(o=at["q"] + 1024))):
+        assert b"overlaps" not in call(**new)[1]  # neighbours are not overlaps (what follows refuses the made-up addresses)
+
+
+def test_more_new_tokens_than_the_write_counts_are_refused(L):
+    c = kdn.PagesC(num_pages=8, page_size=16, rows=4, max_pages=2)
+    st = L.kdn_pages_write(ctypes.byref(c), 1, None, None, (1 << 24) + 1, 2, 64, 64, 1, None, None, None, None, None)
+    assert st == kdn.KDN_ERR_UNSUPPORTED and b"2^24" in L.kdn_last_error()
+
+
 def test_binding_refuses_cpu_tensors_and_bad_shapes():
     x = torch.zeros(1, 2, 4, 16)
     with pytest.raises(ValueError, match="CUDA"):
