@@ -431,3 +431,27 @@ def test_calls_at_once_on_several_streams():
         torch.cuda.synchronize()
         for a, b in zip(alone, together):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype,num", [(torch.bfloat16, 17000), (torch.float32, 17000)])
+def test_a_pool_whose_offsets_pass_32_bits(dtype, num):
+    """Pages at the end of a pool of more than 2^31 elements: written, copied and read as in a small one."""
+    Hkv, page, d, held = 8, 128, 128, 9
+    kp, vp = (torch.empty(num, Hkv, page, d, device=DEV, dtype=dtype) for _ in range(2))
+    assert kp.numel() > 1 << 31
+    used = [num - 1 - 3 * i for i in range(held)]
+    n = held * page - 5
+    books = kdn.Pages(_i32([used]), _i32([n]), _i32([0] * num), page)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(1, Hkv, n, d, generator=g, device=DEV).to(dtype) for _ in range(2))
+    q = torch.randn(1, 16, d, generator=g, device=DEV).to(dtype)
+    kdn.pages_write(books, _i32([0]), k, v, kp, vp)
+    kdn.pages_copy(_i32([[used[0], num - 2], [used[1], 0]]), kp, vp)
+    for x, new in ((kp, k), (vp, v)):
+        seq = x[used].transpose(0, 1).reshape(Hkv, held * page, d)
+        assert torch.equal(seq[:, :n], new[0])
+        assert torch.equal(x[num - 2], x[used[0]]) and torch.equal(x[0], x[used[1]])
+    table = _i32([[num - 2, 0] + used[2:]])
+    o, lse = kdn.paged_attn_step(q, kp, vp, table, books.lens)
+    o1, lse1 = kdn.paged_attn_step(q, kp[used].contiguous(), vp[used].contiguous(), _i32([list(range(held))]), books.lens)
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)

@@ -306,3 +306,24 @@ def test_refusals():
         kdn.window_attn_backward(q, k, v, o, lse, dO.float(), 4)
     with pytest.raises(kdn.KdnError, match="workspace_bytes"):
         kdn.window_attn_backward(q, k, v, o, lse, dO, 4, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("dtype,d,backward", [(torch.bfloat16, 128, True), (torch.float32, 64, False)])
+def test_offsets_beyond_32_bits(dtype, d, backward):
+    """Arrays of more than 2^31 elements: the last head gives what it gives alone, bit for bit (the same tiles in the same
+    order; the other heads' queries and dO are zero and add nothing to dk and dv)."""
+    L = (1 << 17) + 77
+    H = (1 << 31) // (L * d) + 2
+    q = torch.zeros(1, H, L, d, device=DEV, dtype=dtype)
+    assert q.numel() > 1 << 31
+    q1, k, v, dO1 = _inputs(1, 1, 1, L, d, d, dtype, seed=3)
+    q[:, -1:] = q1
+    o, lse = kdn.window_attn(q, k, v, 70)
+    o1, lse1 = kdn.window_attn(q1, k, v, 70)
+    assert torch.equal(o[:, -1:], o1) and torch.equal(lse[:, -1:], lse1)
+    if backward:
+        dO = torch.zeros_like(q)
+        dO[:, -1:] = dO1
+        g = kdn.window_attn_backward(q, k, v, o, lse, dO, 70)
+        g1 = kdn.window_attn_backward(q1, k, v, o1, lse1, dO1, 70)
+        assert torch.equal(g["dq"][:, -1:], g1["dq"]) and torch.equal(g["dk"], g1["dk"]) and torch.equal(g["dv"], g1["dv"])
