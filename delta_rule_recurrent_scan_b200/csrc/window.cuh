@@ -84,44 +84,88 @@ __host__ __device__ __forceinline__ void query_tiles(int j0, int j1, int len, in
   hi = t1 / T + 1;
 }
 
-// The keys' pass of the backward.  The key tiles that hold sinks are seen by every later query; where there are one or two
-// of them their walk is cut into parts of a regular tile's length, whose fp32 sums go to ``part`` and are added in order
-// by a launch of their own.
+// The keys' pass of the backward.  A CTA has a key tile and walks the query tiles that see it; walks that would be far
+// longer than the rest, or too few for the SMs, are cut into parts, one CTA each, whose fp32 sums go to ``part`` and are
+// added in order by a launch of their own.
+//   - Key tiles that hold sinks are seen by every later query: where there are one or two of them they are cut into parts
+//     of the other tiles' length.
+//   - Where the tiles leave half of the SMs without a CTA every tile is cut, as far as SMs and items go.  Backward in all,
+//     whole walks against cut ones: 1 x 8 heads on 2, 2048 tokens, d 128, window 512: 73 -> 45 us; 2 x 8 on 2, 1000 tokens:
+//     92 -> 52; 2 x 16 on 2, 1500 tokens, d 64, 64 sinks: 141 -> 85; fp32, 1 x 2 on 1, 2048 tokens, window 128: 216 -> 57.
 struct KeyPass {
-  int sinks, parts;  // key tiles that are cut, and into how many parts (0, 1: none)
-  float* part;
+  int sinks, parts;  // leading key tiles with a cut of their own, and into how many parts (0, 1: none)
+  int others;        // parts of every other key tile
+  float* part;       // one slot per CTA of a cut tile
   int tile, head;    // of this CTA (key_tile_of)
 };
-// Tiles of K keys walk tiles of Q queries.
+constexpr int kSms = 148;
+
+inline long long key_ctas(const KeyPass& kp, long long heads, int tiles) {
+  return heads * ((long long)kp.sinks * kp.parts + (long long)(tiles - kp.sinks) * kp.others);
+}
+inline int cut_tiles(const KeyPass& kp, int tiles) { return kp.others > 1 ? tiles : kp.sinks; }
+inline long long cut_ctas(const KeyPass& kp, long long heads, int tiles) {
+  return kp.others > 1 ? key_ctas(kp, heads, tiles) : heads * kp.sinks * kp.parts;
+}
+
+// Tiles of K keys walk tiles of Q queries; ``least``: items of a part where every tile is cut.
 template <int K, int Q>
-inline KeyPass key_pass(int H, int Hkv, int L, int window, int n_sink) {
-  const int tiles = (L + K - 1) / K, walk = (L + Q - 1) / Q;
+inline KeyPass key_pass(int B, int H, int Hkv, int L, int window, int n_sink, int least) {
+  const int tiles = (L + K - 1) / K, walk = (L + Q - 1) / Q, G = H / Hkv;
   const int sinks = n_sink <= 0 ? 0 : n_sink < L ? (n_sink - 1) / K + 1 : tiles;
-  KeyPass kp{0, 1, nullptr, 0, 0};
-  if (sinks == 0 || sinks > 2 || sinks >= tiles) return kp;
   const int regular = (window + K - 2) / Q + 2;    // query tiles that see a tile within the window
-  const long long items = (long long)walk * (H / Hkv);
-  long long parts = (walk + regular - 1) / regular;
-  if (parts > 64) parts = 64;
-  if (parts > items / 4) parts = items / 4;        // a part shorter than four tiles is all start-up
-  if (parts < 2) return kp;
-  kp.sinks = sinks, kp.parts = static_cast<int>(parts);
+  const long long heads = (long long)B * Hkv, items = (long long)walk * G;
+  const bool few_sinks = sinks > 0 && sinks <= 2 && sinks < tiles;
+  // parts of a sink tile that make it as long as the other tiles' parts; not shorter than ``shortest``
+  auto sink_parts = [&](int others, int shortest) {
+    long long parts = ((long long)walk * others + regular - 1) / regular;
+    if (parts > 64) parts = 64;
+    if (parts > items / shortest) parts = items / shortest;
+    return parts < 1 ? 1 : static_cast<int>(parts);
+  };
+  KeyPass kp{0, 1, 1, nullptr, 0, 0};
+  if (few_sinks && sink_parts(1, 4) > 1)           // a part shorter than four tiles is all start-up
+    kp.sinks = sinks, kp.parts = sink_parts(1, 4);
+  const long long near = (long long)(regular < walk ? regular : walk) * G;
+  long long most = heads > 0 && tiles > 0 ? kSms / (heads * tiles) : 0, longest = near > items / kp.parts ? near : items / kp.parts;
+  if (sinks == 0) longest = near;
+  if (most > near / least) most = near / least;
+  for (int others = 2; others <= most; ++others) {  // the cut whose longest part is shortest
+    KeyPass all{0, 1, others, nullptr, 0, 0};
+    if (few_sinks) {
+      const long long room = (kSms / heads - (long long)(tiles - sinks) * others) / sinks;
+      const int wanted = sink_parts(others, least), parts = wanted < room ? wanted : static_cast<int>(room);
+      if (parts > others) all.sinks = sinks, all.parts = parts;
+    }
+    const long long sink_part = sinks == 0 ? 0 : items / (all.sinks ? all.parts : others);
+    const long long part = near / others > sink_part ? near / others : sink_part;
+    if (part < longest) kp = all, longest = part;
+  }
   return kp;
 }
-// Key tile and (sequence, k/v head) of CTA x: the cut walks come first (they are the longest), then the other key tiles.
-// True for a cut tile, whose part it is then.
-__device__ __forceinline__ bool key_tile_of(KeyPass& kp, int heads, int tiles, unsigned x, int& part) {
+// Key tile and (sequence, k/v head) of CTA x: the sinks' tiles come first (theirs are the longest walks), then the others.
+// Returns into how many parts the tile is cut; the CTA has part ``part``, whose slot in KeyPass::part is x.
+__device__ __forceinline__ int key_tile_of(KeyPass& kp, int heads, int tiles, unsigned x, int& part) {
   const unsigned cut = (unsigned)heads * kp.sinks * kp.parts;
-  part = 0;
   if (x < cut) {
     part = x % kp.parts, x /= kp.parts;
     kp.tile = x % kp.sinks, kp.head = x / kp.sinks;
-    return true;
+    return kp.parts;
   }
   x -= cut;
+  part = x % kp.others, x /= kp.others;
   const int rest = tiles - kp.sinks;
   kp.tile = kp.sinks + x % rest, kp.head = x / rest;
-  return false;
+  return kp.others;
+}
+// The parts of a cut tile: how many, and the first one's slot.
+__device__ __forceinline__ int parts_of(const KeyPass& kp, int heads, int tiles, size_t head, int tile, size_t& slot) {
+  if (tile < kp.sinks) {
+    slot = (head * kp.sinks + tile) * kp.parts;
+    return kp.parts;
+  }
+  slot = (size_t)heads * kp.sinks * kp.parts + (head * (tiles - kp.sinks) + (tile - kp.sinks)) * kp.others;
+  return kp.others;
 }
 
 }  // namespace window

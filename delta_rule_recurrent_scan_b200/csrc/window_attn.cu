@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kDqRest
 }
 
 // The keys' pass: every query tile that sees the CTA's keys, of every head that shares them, in a fixed order, so the sums
-// of a gradient are the same on every run.  Key tiles with sinks may be cut (window::key_pass).
+// of a gradient are the same on every run.  Tiles may be cut (window::key_pass).
 template <int DK, int DV, int R>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kKeysRest<DK, DV, R>)))
     window_dkdv_kernel(WindowArgs p, KeyPass kp) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kKeysRe
   float* walked = ds_s + kRows * kLP;  // q, then dO; the second set behind them
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int part;
-  const bool is_cut = window::key_tile_of(kp, p.B * p.Hkv, (p.L + kRows - 1) / kRows, blockIdx.x, part);
+  const int parts = window::key_tile_of(kp, p.B * p.Hkv, (p.L + kRows - 1) / kRows, blockIdx.x, part);
   const int tile = kp.tile, h = kp.head % p.Hkv, b = kp.head / p.Hkv;
   const int len = window::seq_len(p, b), j0 = tile * kRows;
   const int G = p.H / p.Hkv;
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kKeysRe
   int lo, hi;
   window::query_tiles<kT>(j0, min(j0 + kRows, len) - 1, len, p.window, p.n_sink, lo, hi);
   const int per = hi - lo, all_items = per * G;  // (head of the group, query tile), query tiles fastest
-  const int first = is_cut ? (int)((long long)all_items * part / kp.parts) : 0;
-  const int last = is_cut ? (int)((long long)all_items * (part + 1) / kp.parts) : all_items;
+  const int first = parts > 1 ? (int)((long long)all_items * part / parts) : 0;
+  const int last = parts > 1 ? (int)((long long)all_items * (part + 1) / parts) : all_items;
   stage<DK, kRows>(k_s, p.k, krow, j0, len, p.in_dtype);
   stage<DV, kRows>(v_s, p.v, krow, j0, len, p.in_dtype);
   const float c = p.scale * kLog2e;
@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kKeysRe
       begin(item + 1);
     }
   }
-  if (is_cut) {  // [tile][part][dk, then dv] of the CTA's rows, fp32
-    float* out = kp.part + (((size_t)kp.head * kp.sinks + tile) * kp.parts + part) * kRows * (DK + DV);
+  if (parts > 1) {  // a slot: [dk, then dv] of the CTA's rows, fp32
+    float* out = kp.part + (size_t)blockIdx.x * kRows * (DK + DV);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       put_row<DK>(out, warp * R + i, dk[i], p.scale, lane, kF32);
@@ -503,21 +503,24 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kKeysRe
 }
 
 // The cut tiles' parts, added in their order; one value per thread.
-__global__ void __launch_bounds__(256) window_sum_parts_kernel(WindowArgs p, KeyPass kp, int rows, int dk, int dv) {
+__global__ void __launch_bounds__(256) window_sum_parts_kernel(WindowArgs p, KeyPass kp, int cut, int rows, int dk, int dv) {
   const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
   const int per = rows * (dk + dv);
   const size_t which = e / per;  // (sequence, k/v head, tile)
-  if (which >= (size_t)p.B * p.Hkv * kp.sinks) return;
+  if (which >= (size_t)p.B * p.Hkv * cut) return;
   int x = static_cast<int>(e % per);
-  const float* from = kp.part + which * kp.parts * per + x;
+  const size_t head = which / cut;
+  const int tile = static_cast<int>(which % cut);
+  size_t slot;
+  const int parts = window::parts_of(kp, p.B * p.Hkv, (p.L + rows - 1) / rows, head, tile, slot);
+  const float* from = kp.part + slot * per + x;
   const bool keys = x < rows * dk;
   if (!keys) x -= rows * dk;
   const int d = keys ? dk : dv;
-  const size_t head = which / kp.sinks;
-  const int j = static_cast<int>(which % kp.sinks) * rows + x / d;
+  const int j = tile * rows + x / d;
   if (j >= window::seq_len(p, static_cast<int>(head / p.Hkv))) return;
   float a = 0.f;
-  for (int i = 0; i < kp.parts; ++i) a += from[(size_t)i * per];
+  for (int i = 0; i < parts; ++i) a += from[(size_t)i * per];
   store_elem(keys ? p.dk : p.dv, (head * p.L + j) * d + x % d, a, p.in_dtype);
 }
 
@@ -530,7 +533,7 @@ cudaError_t run(K kernel, size_t floats, long long ctas, cudaStream_t stream, co
   return cudaGetLastError();
 }
 
-constexpr int kSms = 148;
+using window::kSms;
 long long row_tiles(const WindowArgs& p, int rows, int heads) { return (long long)p.B * heads * ((p.L + rows - 1) / rows); }
 
 template <int DK, int DV, int R>
@@ -548,18 +551,9 @@ cudaError_t dq_pass(const WindowArgs& p, cudaStream_t stream) {
 // Keys per CTA of the keys' pass, in units of the warps: 4 where 8 would leave SMs without a CTA.
 int key_rows(int B, int Hkv, int L) { return (long long)B * Hkv * ((L + 8 * kWarps - 1) / (8 * kWarps)) >= kSms ? 8 : 4; }
 
-// The keys' pass of a call: its sink tiles cut, or, where that leaves SMs without a CTA, the walk of every tile.
-template <int R>
+template <int R>  // keys per warp
 KeyPass cut(int B, int H, int Hkv, int L, int window, int n_sink) {
-  constexpr int kRows = kWarps * R;
-  KeyPass kp = window::key_pass<kRows, kT>(H, Hkv, L, window, n_sink);
-  const long long tiles = (L + kRows - 1) / kRows, heads = (long long)B * Hkv;
-  if (heads * (tiles + (long long)kp.sinks * (kp.parts - 1)) >= kSms) return kp;
-  const int near = (window + kRows - 2) / kT + 2, walk = (L + kT - 1) / kT;  // query tiles that see a tile's keys
-  const long long items = (long long)(H / Hkv) * (n_sink > 0 || near > walk ? walk : near);
-  const long long parts = kSms / (heads * tiles) < items ? kSms / (heads * tiles) : items;
-  if (parts >= 2) kp.sinks = static_cast<int>(tiles), kp.parts = static_cast<int>(parts);
-  return kp;
+  return window::key_pass<kWarps * R, kT>(B, H, Hkv, L, window, n_sink, 1);
 }
 
 template <int DK, int DV, int R>
@@ -567,11 +561,12 @@ cudaError_t keys_pass(const WindowArgs& p, cudaStream_t stream) {
   constexpr int kRows = kWarps * R;
   KeyPass kp = cut<R>(p.B, p.H, p.Hkv, p.L, p.window, p.n_sink);
   kp.part = static_cast<float*>(p.scratch) + ((size_t)p.B * p.H * p.L + 63) / 64 * 64;  // behind delta
-  const long long ctas = (long long)p.B * p.Hkv * kp.sinks * (kp.parts - 1) + row_tiles(p, kRows, p.Hkv);
-  const cudaError_t e = run(window_dkdv_kernel<DK, DV, R>, total<DK, DV, R>(kKeysRest<DK, DV, R>), ctas, stream, p, kp);
-  if (e != cudaSuccess || kp.sinks == 0) return e;
-  const size_t values = (size_t)p.B * p.Hkv * kp.sinks * kRows * (DK + DV);
-  window_sum_parts_kernel<<<(unsigned)((values + 255) / 256), 256, 0, stream>>>(p, kp, kRows, DK, DV);
+  const int heads = p.B * p.Hkv, tiles = (p.L + kRows - 1) / kRows, cut_tiles = window::cut_tiles(kp, tiles);
+  const cudaError_t e = run(window_dkdv_kernel<DK, DV, R>, total<DK, DV, R>(kKeysRest<DK, DV, R>),
+                            window::key_ctas(kp, heads, tiles), stream, p, kp);
+  if (e != cudaSuccess || cut_tiles == 0) return e;
+  const size_t values = (size_t)heads * cut_tiles * kRows * (DK + DV);
+  window_sum_parts_kernel<<<(unsigned)((values + 255) / 256), 256, 0, stream>>>(p, kp, cut_tiles, kRows, DK, DV);
   return cudaGetLastError();
 }
 
@@ -607,7 +602,8 @@ cudaError_t launch_window_attn(int dk, int dv, const WindowArgs& p, cudaStream_t
 size_t window_bwd_scratch_bytes(int B, int H, int Hkv, int L, int dk, int dv, int window, int n_sink) {
   const int w = window < L ? window : L, s = n_sink < L ? n_sink : L, rows = key_rows(B, Hkv, L) * kWarps;
   const KeyPass kp = rows == 8 * kWarps ? cut<8>(B, H, Hkv, L, w, s) : cut<4>(B, H, Hkv, L, w, s);
-  return (((size_t)B * H * L + 63) / 64 * 64 + (size_t)B * Hkv * kp.sinks * kp.parts * rows * (dk + dv)) * sizeof(float);
+  const size_t slots = (size_t)window::cut_ctas(kp, (long long)B * Hkv, (L + rows - 1) / rows);
+  return (((size_t)B * H * L + 63) / 64 * 64 + slots * rows * (dk + dv)) * sizeof(float);
 }
 
 cudaError_t launch_window_attn_backward(int dk, int dv, const WindowArgs& p, cudaStream_t stream) {

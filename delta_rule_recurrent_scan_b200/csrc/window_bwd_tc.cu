@@ -17,7 +17,7 @@
 // A warpgroup takes half of a tile's columns: thread = (lane, half).  One load warp (TMA rings), one warp whose first
 // lane issues the products.  Rows behind a sequence's end are zeroed in shared memory.
 //
-// Key tiles with sinks may be cut into parts (window::key_pass); part: [B, Hkv, sinks, parts, 2, 128, D].
+// Key tiles may be cut into parts (window::key_pass); a part's slot: [2 (dv, dk), 128, D].
 #include "window_tc.cuh"
 
 namespace kdn {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
   int part;
-  const bool is_cut = window::key_tile_of(kp, bh, tiles, blockIdx.x, part);
+  const int parts = window::key_tile_of(kp, bh, tiles, blockIdx.x, part);
   const int tile = kp.tile, kvh = kp.head % p.Hkv, b = kp.head / p.Hkv;
   const int len = window::seq_len(p, b), j0 = tile * kT;
   if (p.zero_rest && part == 0 && j0 + kT > len) {
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int lo, hi;
   window::query_tiles<kT>(j0, min(j0 + kT, len) - 1, len, p.window, p.n_sink, lo, hi);
   const int per = hi - lo, all = per * G;  // (head of the group, query tile), query tiles fastest
-  const int first = is_cut ? (int)((long long)all * part / kp.parts) : 0;
-  const int n = (is_cut ? (int)((long long)all * (part + 1) / kp.parts) : all) - first;
+  const int first = parts > 1 ? (int)((long long)all * part / parts) : 0;
+  const int n = (parts > 1 ? (int)((long long)all * (part + 1) / parts) : all) - first;
 
   if (tid == 0) {
     sm100::mbar_init(&kv_full, 1);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t t_out = (half == 0 ? t_dv : t_dk) + lanes;
       const float f = half == 0 ? 1.f : p.scale;
       const size_t at = ((size_t)(b * p.Hkv + kvh) * p.L + j) * D;
-      float* cut_out = kp.part + ((((size_t)(b * p.Hkv + kvh) * kp.sinks + tile) * kp.parts + part) * 2 + half) * kT * D + key * D;
+      float* cut_out = kp.part + ((size_t)blockIdx.x * 2 + half) * kT * D + key * D;
       const bool wide = is_wide(half == 0 ? p.dv : p.dk);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half == 0 ? p.dv : p.dk) + at;
 #pragma unroll 1
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) a[e] = 0.f;
         }
-        if (is_cut) {
+        if (parts > 1) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<float4*>(cut_out + u + 4 * e) = make_float4(a[4 * e] * f, a[4 * e + 1] * f, a[4 * e + 2] * f, a[4 * e + 3] * f);
@@ -354,19 +354,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // The cut tiles' parts, added in their order; a thread has 8 consecutive values.
 template <int D>
-__global__ void __launch_bounds__(256) window_join_kernel(WindowArgs p, KeyPass kp) {
+__global__ void __launch_bounds__(256) window_join_kernel(WindowArgs p, KeyPass kp, int cut) {
   constexpr int kWords = 2 * kT * D / 8;
   const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
   const size_t which = e / kWords;  // (sequence, k/v head, tile)
-  if (which >= (size_t)p.B * p.Hkv * kp.sinks) return;
+  if (which >= (size_t)p.B * p.Hkv * cut) return;
   const int w = static_cast<int>(e % kWords), half = w / (kT * D / 8), key = w / (D / 8) % kT, c = w % (D / 8) * 8;
-  const int tile = static_cast<int>(which % kp.sinks);
-  const size_t head = which / kp.sinks;
+  const int tile = static_cast<int>(which % cut);
+  const size_t head = which / cut;
   const int j = tile * kT + key;
   if (j >= window::seq_len(p, static_cast<int>(head / p.Hkv))) return;
-  const float* from = kp.part + which * kp.parts * 2 * kT * D + (half * kT + key) * D + c;
+  size_t slot;
+  const int parts = window::parts_of(kp, p.B * p.Hkv, (p.L + kT - 1) / kT, head, tile, slot);
+  const float* from = kp.part + slot * 2 * kT * D + (half * kT + key) * D + c;
   float a[8] = {};
-  for (int i = 0; i < kp.parts; ++i) {
+  for (int i = 0; i < parts; ++i) {
     const float4 u = *reinterpret_cast<const float4*>(from + (size_t)i * 2 * kT * D);
     const float4 v = *reinterpret_cast<const float4*>(from + (size_t)i * 2 * kT * D + 4);
     a[0] += u.x, a[1] += u.y, a[2] += u.z, a[3] += u.w, a[4] += v.x, a[5] += v.y, a[6] += v.z, a[7] += v.w;
@@ -661,21 +663,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Query tiles of a part where every key tile is cut: 1 and 2 measure the same, with 4 short sequences lose (1 of 200, 3
+// heads on 1, d 128: 47.7 against 38.7 us).
+constexpr int kLeast = 2;
 struct Layout {
   size_t rows, dO, part, end;  // byte offsets in the scratch
 };
+KeyPass cut(int B, int H, int Hkv, int L, int window, int n_sink) {
+  return window::key_pass<kT, kT>(B, H, Hkv, L, window, n_sink, kLeast);
+}
 Layout layout(int B, int H, int Hkv, int L, int D, int out_dtype, const KeyPass& kp) {
   Layout l{};
   const size_t tokens = (size_t)B * H * L;
   l.rows = 0, l.dO = round256(tokens * sizeof(float2));
   l.part = l.dO + (out_dtype == kF32 ? round256(tokens * D * 2) : 0);
-  l.end = l.part + (kp.sinks ? round256((size_t)B * Hkv * kp.sinks * kp.parts * 2 * kT * D * sizeof(float)) : 0);
+  l.end = l.part + (size_t)window::cut_ctas(kp, (long long)B * Hkv, (L + kT - 1) / kT) * 2 * kT * D * sizeof(float);
   return l;
 }
 
 template <int D>
 cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
-  KeyPass kp = window::key_pass<kT, kT>(p.H, p.Hkv, p.L, p.window, p.n_sink);
+  KeyPass kp = cut(p.B, p.H, p.Hkv, p.L, p.window, p.n_sink);
   const Layout l = layout(p.B, p.H, p.Hkv, p.L, D, p.out_dtype, kp);
   char* scratch = static_cast<char*>(p.scratch);
   float2* rows = reinterpret_cast<float2*>(scratch + l.rows);
@@ -698,7 +706,8 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(window_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long keys = (long long)bh * (kp.sinks * kp.parts + tiles - kp.sinks);
+  const long long keys = window::key_ctas(kp, bh, tiles);
+  const int cut_tiles = window::cut_tiles(kp, tiles);
   QueryPass qp;
   qp.works = (unsigned)((long long)p.B * p.H * tiles), qp.tiles = tiles;
   qp.group = make_divisor(p.H / p.Hkv), qp.kv_heads = make_divisor(p.Hkv), qp.batch = make_divisor(p.B);
@@ -709,16 +718,16 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   window_dkdv_tc_kernel<D><<<(unsigned)keys, kTcThreads, key_smem, stream>>>(tq, tk, tv, td, p, rows, kp);
   e = cudaGetLastError();
-  if (e != cudaSuccess || kp.sinks == 0) return e;
-  const size_t words = (size_t)bh * kp.sinks * 2 * kT * D / 8;
-  window_join_kernel<D><<<(unsigned)((words + 255) / 256), 256, 0, stream>>>(p, kp);
+  if (e != cudaSuccess || cut_tiles == 0) return e;
+  const size_t words = (size_t)bh * cut_tiles * 2 * kT * D / 8;
+  window_join_kernel<D><<<(unsigned)((words + 255) / 256), 256, 0, stream>>>(p, kp, cut_tiles);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t window_bwd_tc_scratch_bytes(int B, int H, int Hkv, int L, int d, int out_dtype, int window, int n_sink) {
-  return layout(B, H, Hkv, L, d, out_dtype, window::key_pass<kT, kT>(H, Hkv, L, window < L ? window : L, n_sink < L ? n_sink : L)).end;
+  return layout(B, H, Hkv, L, d, out_dtype, cut(B, H, Hkv, L, window < L ? window : L, n_sink < L ? n_sink : L)).end;
 }
 
 cudaError_t launch_window_bwd_tc(int d, const WindowArgs& p, cudaStream_t stream) {

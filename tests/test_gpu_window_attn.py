@@ -108,6 +108,15 @@ def test_sinks_of_a_long_sequence(dtype, d, n_sink, H, Hkv):
     _check(*_inputs(4, H, Hkv, 1700, d, d, dtype, seed=16), 60, n_sink, lens)
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.bfloat16, 64), (torch.bfloat16, 128)])
+@pytest.mark.parametrize("H,Hkv,window,n_sink", [(4, 1, 1500, 0), (8, 1, 100, 5), (4, 2, 300, 150), (8, 1, 200, 700), (3, 1, 1, 0)])
+@pytest.mark.parametrize("lens", [[1500], [1500, 70, 0]])
+def test_few_key_tiles_whose_walks_are_cut(dtype, d, H, Hkv, window, n_sink, lens):
+    """Fewer key tiles than half of the SMs: every walk is cut, the sinks' into more parts than the others; without a
+    window the last tiles have fewer query tiles than parts, and short sequences leave parts empty."""
+    _check(*_inputs(len(lens), H, Hkv, 1500, d, d, dtype, seed=18), window, n_sink, torch.tensor(lens, dtype=torch.int32, device=DEV))
+
+
 @pytest.mark.parametrize("dtype,d", [(torch.float32, 32), (torch.float32, 16), (torch.bfloat16, 64), (torch.bfloat16, 128)])
 @pytest.mark.parametrize("B,H,Hkv", [(5, 12, 4), (7, 7, 7)])
 def test_more_work_than_multiprocessors(dtype, d, B, H, Hkv):
