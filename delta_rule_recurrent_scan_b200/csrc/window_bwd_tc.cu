@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kNP = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t q_full, q_empty, k_full[kSlots], k_empty[kSlots], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready[2], done, last;
+  __shared__ uint64_t q_full, q_empty, k_full[kSlots], k_empty[kSlots], v_full[2], v_empty[2], s_ready, s_free, dp_ready[2], ds_ready[2], delta_ready, done, last;
   __shared__ uint32_t tmem_base;
   __shared__ float delta_s[2][kT];
 
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::mbar_init(&v_full[i], 1), sm100::mbar_init(&v_empty[i], 1);
       sm100::mbar_init(&dp_ready[i], 1), sm100::mbar_init(&ds_ready[i], 8);
     }
-    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&s_free, 8);
+    sm100::mbar_init(&s_ready, 1), sm100::mbar_init(&s_free, 8), sm100::mbar_init(&delta_ready, 8);
     sm100::mbar_init(&done, 1), sm100::mbar_init(&last, 1);
     sm100::fence_mbar_init();
   }
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
     const bool wide = is_wide(p.dq);
-    unsigned c = 0, works = 0;
+    unsigned c = 0, works = 0, sweeps = 0;
     for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
       const unsigned x = nth_work(r);
       if (x >= qp.works) continue;
@@ -608,12 +608,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sm100::tc_fence_before();
           warp_arrive(&ds_ready[c & 1]);
           if (it + 1 == w.n) {  // the row's other half of the columns is the other warpgroup's
+            // Written again in this CTA's next first sweep only, behind a step whose scores wait (s_free) until all eight
+            // warps have gone on from here.
             delta_s[half][tid & 127] = sum.x + sum.y;
-            chunk::named_sync(1, 256);
+            warp_arrive(&delta_ready);
+            fine = warp_wait(&delta_ready, sweeps & 1);
+            if (!fine) break;
+            ++sweeps;
             const float delta = delta_s[0][tid & 127] + delta_s[1][tid & 127];
             d2 = make_float2(-delta, -delta);
             if (half == 0 && t < w.len) rows[(size_t)w.qrow * p.L + t].y = -delta;
-            chunk::named_sync(1, 256);  // both have read it
           }
           continue;
         }

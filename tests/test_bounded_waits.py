@@ -1,0 +1,51 @@
+"""Waits of the windowed-attention kernels on the tensor cores are bounded, so that a step that never comes ends in a
+status and not in a hang.  Read from the source: a kernel that waits for ever must not run."""
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "delta_rule_recurrent_scan_b200", "csrc")
+FILES = ["window_attn_tc.cu", "window_bwd_tc.cu", "window_tc.cuh"]
+
+
+def _code(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def _kernels(text):
+    """(name, body) of every __global__ function."""
+    for m in re.finditer(r"__global__[^;{]*?(\w+)\((?=const|WindowArgs)", text):
+        at = text.index("{", m.end())
+        depth, end = 0, at
+        while True:
+            depth += {"{": 1, "}": -1}.get(text[end], 0)
+            end += 1
+            if depth == 0:
+                break
+        yield m.group(1), text[at:end]
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_no_barrier_waits_for_warps_that_may_have_given_up(name):
+    """A warp whose bounded wait gives up leaves its role at once.  Every barrier that counts threads (named ones and
+    __syncthreads) would wait for it for ever, except before the roles begin and where all of them end."""
+    text = _code(name)
+    assert "named_sync" not in text and "bar.sync" not in text and "barrier.sync" not in text
+    assert re.findall(r"mbarrier\.\w+", text) == [], "waits go through sm100::mbar_wait_bounded"
+    assert "mbar_try_wait" not in text
+    for kernel, body in _kernels(text):
+        if "mbar_wait_bounded" not in body and "warp_wait" not in body:
+            continue
+        roles = body.index("bool fine = true;")
+        assert body[:roles].count("__syncthreads()") == 1, kernel
+        after = body[roles:]
+        assert after.count("__syncthreads()") == 1, kernel
+        assert not re.search(r"\bwarp_wait|mbar_wait_bounded|\bfor \(", after[after.index("__syncthreads()"):]), kernel
+
+
+def test_the_scan_finds_the_kernels():
+    names = [k for f in FILES for k, body in _kernels(_code(f)) if "warp_wait" in body]
+    assert names == ["window_fwd_tc_kernel", "window_dkdv_tc_kernel", "window_dq_tc_kernel"]
