@@ -14,6 +14,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "bounded_wait.h"
+
 namespace kdn {
 namespace sm100 {
 
@@ -65,12 +67,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Bounded wait: gives up after ``max_cycles`` SM clocks and returns false.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, long long max_cycles) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > max_cycles) return false;
-  }
-  return true;
+  return wait_bounded([=] { return mbar_try_wait(bar, parity); }, [] { return clock64(); }, max_cycles);
 }
 
 // --------------------------------------------------------------------------- TMA

@@ -3,6 +3,8 @@ status and not in a hang.  Read from the source: a kernel that waits for ever mu
 
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -49,3 +51,20 @@ def test_no_barrier_waits_for_warps_that_may_have_given_up(name):
 def test_the_scan_finds_the_kernels():
     names = [k for f in FILES for k, body in _kernels(_code(f)) if "warp_wait" in body]
     assert names == ["window_fwd_tc_kernel", "window_dkdv_tc_kernel", "window_dq_tc_kernel"]
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_the_last_word_of_a_bounded_wait_is_a_try(tmp_path):
+    """The loop behind every bounded wait, compiled for the host against a fake clock."""
+    exe = tmp_path / "bounded_wait_check"
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "native", "bounded_wait_check.cpp")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", CSRC, src, "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_mbarrier_waits_use_that_loop():
+    text = _code("sm100.cuh")
+    assert text.count("mbarrier.try_wait") == 1 and text.count("mbar_try_wait(") == 2
+    body = text[text.index("bool mbar_wait_bounded"):]
+    assert "return wait_bounded(" in body[:body.index("}\n\n")]
