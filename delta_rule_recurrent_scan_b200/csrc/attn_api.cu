@@ -94,11 +94,15 @@ kdn_status check_pages(const kdn_pages* p) {
   return KDN_OK;
 }
 
+// The books' workspace: the status word, scratch, and a word per row for refused reservations.
+size_t refused_at(const kdn_pages* p) { return kStatusBytes + round256(kdn::pages_scratch_ints(p->num_pages) * sizeof(int)); }
+
 kdn::PagesArgs pages_args(const kdn_pages* p, void* ws) {
-  kdn::PagesArgs a{p->num_pages, p->page_size, p->rows, p->max_pages, p->table, p->lens, p->refs, nullptr, nullptr};
+  kdn::PagesArgs a{p->num_pages, p->page_size, p->rows, p->max_pages, p->table, p->lens, p->refs, nullptr, nullptr, nullptr};
   if (ws != nullptr) {
     a.status = static_cast<unsigned*>(ws);
     a.scratch = reinterpret_cast<int*>(static_cast<char*>(ws) + kStatusBytes);
+    a.refused = reinterpret_cast<int*>(static_cast<char*>(ws) + refused_at(p));
   }
   return a;
 }
@@ -125,6 +129,31 @@ kdn_status check_pool(int kv_heads, int dk, int dv, kdn_dtype dtype) {
   if (!pool_dim(dk) || !pool_dim(dv)) return fail(KDN_ERR_UNSUPPORTED, "dk and dv must be 16, 32, 64 or 128");
   if (dtype != KDN_F32 && dtype != KDN_BF16) return fail(KDN_ERR_INVALID_ARG, "bad dtype");
   return KDN_OK;
+}
+
+// workspace: of the books, or NULL to write whatever the last reservations came to.
+kdn_status write_pages(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens, int kv_heads, int dk,
+                       int dv, kdn_dtype dtype, const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                       void* workspace, void* stream) {
+  KDN_TRY(check_pages(pages));
+  if (n < 0 || tokens < 0) return fail(KDN_ERR_INVALID_ARG, "n and tokens must be >= 0");
+  if (tokens > 1 << 24) return fail(KDN_ERR_UNSUPPORTED, "tokens must be at most 2^24");
+  KDN_TRY(check_pool(kv_heads, dk, dv, dtype));
+  const bool none = n == 0 || tokens == 0;
+  KDN_TRY(check_ptr(pages->table, "table", 4, false));
+  KDN_TRY(check_ptr(pages->lens, "lens", 4, false));
+  KDN_TRY(check_ptr(rows, "rows", 4, none));
+  KDN_TRY(check_ptr(counts, "counts", 4, true));
+  KDN_TRY(check_ptr(k_new, "k_new", 16, none));
+  KDN_TRY(check_ptr(v_new, "v_new", 16, none));
+  KDN_TRY(check_ptr(k_pages, "k_pages", 16, false));
+  KDN_TRY(check_ptr(v_pages, "v_pages", 16, false));
+  if (none) return ok();
+  DeviceGuard guard;
+  KDN_TRY(use_device_of(k_pages, guard));
+  const int es = (int)elem_bytes(dtype);
+  const kdn::PagesWrite w{n, kv_heads, tokens, dk * es, dv * es, rows, counts, k_new, v_new, k_pages, v_pages};
+  return cuda_status(kdn::launch_pages_write(pages_args(pages, workspace), w, (cudaStream_t)stream), "page write launch");
 }
 
 }  // namespace
@@ -213,7 +242,7 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
 
 size_t kdn_pages_workspace_bytes(const kdn_pages* pages) {
   if (!pages_sizes_ok(pages)) return 0;
-  return kStatusBytes + round256(kdn::pages_scratch_ints(pages->num_pages) * sizeof(int));
+  return refused_at(pages) + round256((size_t)pages->rows * sizeof(int));
 }
 
 kdn_status kdn_pages_reserve(const kdn_pages* pages, int n, const int* rows, const int* counts, int count,
@@ -275,25 +304,17 @@ kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int page_size,
 kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens, int kv_heads,
                            int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new, void* k_pages,
                            void* v_pages, void* stream) {
+  return write_pages(pages, n, rows, counts, tokens, kv_heads, dk, dv, dtype, k_new, v_new, k_pages, v_pages, nullptr, stream);
+}
+
+kdn_status kdn_pages_write_reserved(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens,
+                                    int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new,
+                                    void* k_pages, void* v_pages, const void* workspace, size_t workspace_bytes,
+                                    void* stream) {
   KDN_TRY(check_pages(pages));
-  if (n < 0 || tokens < 0) return fail(KDN_ERR_INVALID_ARG, "n and tokens must be >= 0");
-  if (tokens > 1 << 24) return fail(KDN_ERR_UNSUPPORTED, "tokens must be at most 2^24");
-  KDN_TRY(check_pool(kv_heads, dk, dv, dtype));
-  const bool none = n == 0 || tokens == 0;
-  KDN_TRY(check_ptr(pages->table, "table", 4, false));
-  KDN_TRY(check_ptr(pages->lens, "lens", 4, false));
-  KDN_TRY(check_ptr(rows, "rows", 4, none));
-  KDN_TRY(check_ptr(counts, "counts", 4, true));
-  KDN_TRY(check_ptr(k_new, "k_new", 16, none));
-  KDN_TRY(check_ptr(v_new, "v_new", 16, none));
-  KDN_TRY(check_ptr(k_pages, "k_pages", 16, false));
-  KDN_TRY(check_ptr(v_pages, "v_pages", 16, false));
-  if (none) return ok();
-  DeviceGuard guard;
-  KDN_TRY(use_device_of(k_pages, guard));
-  const int es = (int)elem_bytes(dtype);
-  const kdn::PagesWrite w{n, kv_heads, tokens, dk * es, dv * es, rows, counts, k_new, v_new, k_pages, v_pages};
-  return cuda_status(kdn::launch_pages_write(pages_args(pages, nullptr), w, (cudaStream_t)stream), "page write launch");
+  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_pages_workspace_bytes(pages)));
+  return write_pages(pages, n, rows, counts, tokens, kv_heads, dk, dv, dtype, k_new, v_new, k_pages, v_pages,
+                     const_cast<void*>(workspace), stream);
 }
 
 size_t kdn_paged_step_workspace_bytes(const kdn_pages* pages, int n, int H, int kv_heads, int dk, int dv,

@@ -294,6 +294,7 @@ struct PagesArgs {
   int* refs;            // [num_pages] table entries that name the page
   unsigned* status;
   int* scratch;         // pages_scratch_ints(num_pages)
+  int* refused;         // [rows]: 1 where the row's last reservation was refused; or nullptr
 };
 // The newest ``tokens`` (or counts[i]) tokens of the listed rows.
 struct PagesWrite {

@@ -8,7 +8,8 @@
 // The books are small (4 bytes per page and table entry) and the steps depend on each other (validate, count, find
 // free pages, hand out), so one CTA of 1024 threads does each call: the searches stream refs at 16 KB per step.  A
 // call that cannot be served as a whole (a row out of range, listed twice, too long, or no page left) changes nothing
-// and says so in the status word, which this CTA stores itself: no separate clearing launch.
+// and says so in the status word, which this CTA stores itself: no separate clearing launch.  The host may well enqueue the
+// write of the new tokens before it knows, so a refused reservation also marks its rows, and the write passes over them.
 //
 // The data movers are bandwidth-bound copies of 16-byte words.
 #include "common.cuh"
@@ -122,7 +123,11 @@ __global__ void __launch_bounds__(kBook, 1) pages_reserve_kernel(PagesArgs p, in
   }
   __syncthreads();
   if (threadIdx.x == 0) *p.status = s.bad;
-  if (s.bad) return;
+  if (s.bad) {  // the write that was to follow would fall on the rows' older tokens
+    for (int i = threadIdx.x; i < n; i += kBook)
+      if (rows[i] >= 0 && rows[i] < p.rows) p.refused[rows[i]] = 1;
+    return;
+  }
   int given = 0;
   for (int base = 0; base < n; base += kBook) {
     const int i = base + threadIdx.x;
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kBook, 1) pages_reserve_kernel(PagesArgs p, in
       p.table[(size_t)r * p.max_pages + had + k] = page;
       p.refs[page] = 1;
     }
-    if (i < n) p.lens[r] = len + c;
+    if (i < n) p.lens[r] = len + c, p.refused[r] = 0;
   }
 }
 
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kBook, 1) pages_fork_kernel(PagesArgs p, int n
         else atomicOr(&s.bad, kStatusInvalid);
       }
       moves[i] = mv;
-      p.lens[dst[i]] = len;
+      p.lens[dst[i]] = len, p.refused[dst[i]] = 0;
     }
   }
   // the full pages are shared: one warp per row
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kBook, 1) pages_free_kernel(PagesArgs p, int n
     for (int i = threadIdx.x >> 5; i < n; i += kBook / 32) {
       const int r = rows[i];
       int len = 0;
-      if (lane == 0) len = atomicExch(&p.lens[r], 0);  // a row listed twice is freed once
+      if (lane == 0) len = atomicExch(&p.lens[r], 0), p.refused[r] = 0;  // a row listed twice is freed once
       len = __shfl_sync(0xffffffffu, len, 0);
       const int held = min(pages_of(p, min(len, 0x7fffffff - p.page_size)), p.max_pages);
       for (int e = lane; e < held; e += 32) {
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(256) pages_write_kernel(PagesArgs p, PagesWrit
     if (!keys) c -= w.tokens * kw;
     const int words = keys ? kw : vw, t = c / words, word = c % words;
     const int r = w.rows[i], count = w.counts ? w.counts[i] : w.tokens;
-    if (r < 0 || r >= p.rows || t >= count || count > w.tokens) continue;
+    if (r < 0 || r >= p.rows || t >= count || count > w.tokens || (p.refused && p.refused[r])) continue;
     const int pos = p.lens[r] - count + t;
     if (pos < 0 || pos / p.page_size >= p.max_pages) continue;
     const int page = p.table[(size_t)r * p.max_pages + pos / p.page_size];

@@ -117,6 +117,7 @@ def lib() -> ctypes.CDLL:
     L.kdn_pages_workspace_bytes.argtypes = [pages]
     L.kdn_pages_copy.argtypes = [i, vp, i, i, i, i, i, i, vp, vp, vp]
     L.kdn_pages_write.argtypes = [pages, i, vp, vp, i, i, i, i, i, vp, vp, vp, vp, vp]
+    L.kdn_pages_write_reserved.argtypes = [pages, i, vp, vp, i, i, i, i, i, vp, vp, vp, vp, vp, sz, vp]
     L.kdn_paged_attn_step.argtypes = [pages, i, vp, i, i, i, i, i, i, vp, vp, vp, i, i, f, vp, vp, vp, sz, vp]
     L.kdn_paged_step_workspace_bytes.argtypes = [pages] + [i] * 8
     for name in ("kdn_window_workspace_bytes", "kdn_pages_workspace_bytes", "kdn_paged_step_workspace_bytes"):
@@ -636,8 +637,8 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
 class Pages:
     """The books of a paged cache (kdn_pages): table [rows, max_pages], lens [rows] and refs [num_pages], int32.  One
     set serves every layer; a layer's pages are k_pages [num_pages, kv_heads, page_size, d_k] and v_pages.
-    ``workspace`` (allocated with the books) holds the status of the last book-keeping call:
-    read_device_status(pages.workspace)."""
+    ``workspace`` (allocated with the books; one given here has to hold zeros) has the status of the last book-keeping
+    call, read_device_status(pages.workspace), and which rows' last reservation was refused."""
     table: torch.Tensor
     lens: torch.Tensor
     refs: torch.Tensor
@@ -645,8 +646,13 @@ class Pages:
     workspace: torch.Tensor | None = None
 
     def __post_init__(self):
+        self._own = None
         if self.workspace is None and self.table.is_cuda:
-            self.workspace = _scratch(None, lib().kdn_pages_workspace_bytes(self._c()), self.table.device)
+            self._allocate(self._c())
+
+    def _allocate(self, c):
+        self.workspace = torch.zeros(max(256, lib().kdn_pages_workspace_bytes(c)), dtype=torch.uint8, device=self.table.device)
+        self._own = c.num_pages, c.rows
 
     def _c(self, dev=None):
         table, lens, refs = self.table, self.lens, self.refs
@@ -675,11 +681,15 @@ def _list(t, name, dev):
 
 def _books(pages):
     c = pages._c()
+    if pages._own not in (None, (c.num_pages, c.rows)):  # the books were exchanged for larger or smaller ones
+        pages._allocate(c)
     return c, pages.table.device, pages.workspace
 
 
 def pages_reserve(pages, rows, counts, stream=None):
-    """Adds tokens to the listed rows (int32 [n]), with the pages they need: ``counts`` each, or counts[i] (int32 [n])."""
+    """Adds tokens to the listed rows (int32 [n]), with the pages they need: ``counts`` each, or counts[i] (int32 [n]).
+    Refused as a whole where there is no room: read_device_status(pages.workspace) says so (it waits for the stream), and
+    pages_write passes over the rows until a reservation succeeds."""
     c, dev, ws = _books(pages)
     _list(rows, "rows", dev)
     each = isinstance(counts, torch.Tensor)
@@ -760,10 +770,11 @@ def pages_copy(moves, k_pages, v_pages, stream=None):
 
 def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream=None):
     """Writes the newest tokens of the listed rows (added by pages_reserve) into one layer's pages: k_new
-    [n, kv_heads, tokens, d_k] and v_new; of entry i the first counts[i] (or all) are the row's last counts[i]."""
+    [n, kv_heads, tokens, d_k] and v_new; of entry i the first counts[i] (or all) are the row's last counts[i].  Rows whose
+    last reservation was refused are left as they are."""
     dev = pages.table.device
     num, Hkv, page, dk, dv = _pool(k_pages, v_pages, dev)
-    c = pages._c()
+    c, _, ws = _books(pages)
     if num != c.num_pages or page != pages.page_size:
         raise ValueError(f"k_pages holds {num} pages of {page} tokens, the books {c.num_pages} of {pages.page_size}")
     _list(rows, "rows", dev)
@@ -775,10 +786,10 @@ def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream
     _need(v_new, "v_new", (n, Hkv, T, dv), k_pages.dtype, dev)
     if counts is not None:
         _need(counts, "counts", (n,), torch.int32, dev)
-    st = lib().kdn_pages_write(c, n, _at(rows), _at(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype],
-                               _at(k_new), _at(v_new), _at(k_pages), _at(v_pages), _stream_of(stream, dev))
+    st = lib().kdn_pages_write_reserved(c, n, _at(rows), _at(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype], _at(k_new),
+                                        _at(v_new), _at(k_pages), _at(v_pages), _at(ws), ws.numel(), _stream_of(stream, dev))
     if st:
-        _check(st, "kdn_pages_write")
+        _check(st, "kdn_pages_write_reserved")
 
 
 def paged_attn_step(q, k_pages, v_pages, table, lens, rows=None, window=0, n_sink=0, scale=None, o=None, lse=None,

@@ -345,10 +345,12 @@ typedef struct kdn_pages {
 /* Book-keeping calls.  Each is carried out as a whole or, when it cannot be, changes nothing and sets the status
  * word (kdn_read_device_status): KDN_ERR_INVALID_ARG for a row out of range or listed twice, KDN_ERR_CAPACITY
  * when no page or no table entry is left.  New pages are the lowest free ones, in the order of the list.  rows
- * are device arrays of n int32.  workspace: kdn_pages_workspace_bytes(pages) bytes; asynchronous; the calls on
- * one cache must be ordered (one stream, or events).
+ * are device arrays of n int32.  workspace: kdn_pages_workspace_bytes(pages) bytes, one for all calls on a cache and set
+ * to zero once with its books; asynchronous; the calls on one cache must be ordered (one stream, or events).
  *   reserve  adds counts[i] (counts NULL: count) tokens to row rows[i], with the pages they need; a row may be
- *            listed once.  The tokens themselves are written with kdn_pages_write.
+ *            listed once.  The tokens themselves are written with kdn_pages_write_reserved.  A call that is refused is
+ *            noted in the workspace for each of its rows, until a reservation (of any number of tokens, none too) of the
+ *            row succeeds, or the row is freed or made by a fork.
  *   fork     makes the empty row dst_rows[i] a copy of src_rows[i]: full pages are shared, a part-filled last page
  *            gets a page of its own, and moves[i] = (old page, new page), or (-1, -1), says what kdn_pages_copy has
  *            to copy before either row is written or read again.  A source may be listed often; a destination once,
@@ -377,10 +379,17 @@ KDN_EXPORT kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int
 /* Writes the newest tokens of rows rows[0..n) into one layer's pages, after kdn_pages_reserve has added them:
  * k_new [n, kv_heads, tokens, d_k], v_new [n, kv_heads, tokens, d_v]; of entry i the first counts[i] (NULL: tokens,
  * at most 2^24) are the last counts[i] tokens of the row.  Entries whose row, count or page is out of range are
- * skipped; of a row listed twice either entry may be the one that stays. */
+ * skipped; of a row listed twice either entry may be the one that stays.
+ * kdn_pages_write_reserved also skips rows whose last reservation was refused, as the books' workspace says: their last
+ * tokens are older ones, in pages that other rows may share.  kdn_pages_write does not ask: it is for callers that have
+ * read the status word, or that write tokens again. */
 KDN_EXPORT kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens,
                            int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new,
                            void* k_pages, void* v_pages, void* stream);
+KDN_EXPORT kdn_status kdn_pages_write_reserved(const kdn_pages* pages, int n, const int* rows, const int* counts,
+                                    int tokens, int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new,
+                                    const void* v_new, void* k_pages, void* v_pages, const void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* One new token per sequence against the paged cache, next to kdn_decode_step's against the resident state.
  * Sequence i is row rows[i] (rows NULL: i) of the table, its new token the row's last, already written.

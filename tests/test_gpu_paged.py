@@ -455,3 +455,122 @@ def test_a_pool_whose_offsets_pass_32_bits(dtype, num):
     o, lse = kdn.paged_attn_step(q, kp, vp, table, books.lens)
     o1, lse1 = kdn.paged_attn_step(q, kp[used].contiguous(), vp[used].contiguous(), _i32([list(range(held))]), books.lens)
     assert torch.equal(o, o1) and torch.equal(lse, lse1)
+
+
+# ------------------------------------------------------------------------------------------ refused calls
+
+def _full_pool(page=4, Hkv=2, d=64, dtype=torch.bfloat16):
+    """Rows 0 and 1 share two full pages, row 2 holds the rest of the pool: no page is left."""
+    g = torch.Generator(device=DEV).manual_seed(40)
+    pages = kdn.make_pages(6, page, 4, 6)
+    k, v = (torch.zeros(6, Hkv, page, d, device=DEV, dtype=dtype) for _ in range(2))
+    new = lambda n, t: [torch.randn(n, Hkv, t, d, generator=g, device=DEV).to(dtype) for _ in range(2)]  # noqa: E731
+    kdn.pages_reserve(pages, _i32([0]), 2 * page)
+    kdn.pages_write(pages, _i32([0]), *new(1, 2 * page), k, v)
+    kdn.pages_copy(kdn.pages_fork(pages, _i32([0]), _i32([1])), k, v)
+    kdn.pages_reserve(pages, _i32([2]), 4 * page)
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK and bool((pages.refs > 0).all())
+    return pages, k, v, new
+
+
+def _rows_hold(pages, k, v, row, kn, vn):
+    """The newest tokens of a row are kn, vn [Hkv, T, d]."""
+    page, T = pages.page_size, kn.shape[1]
+    j = torch.arange(T, device=DEV) + int(pages.lens[row]) - T
+    at = pages.table[row].long()[j // page], j % page
+    return torch.equal(k[at[0], :, at[1]].transpose(0, 1), kn) and torch.equal(v[at[0], :, at[1]].transpose(0, 1), vn)
+
+
+@pytest.mark.parametrize("counts", [1, [1, 1]])
+def test_a_write_behind_a_refused_reservation_changes_nothing(counts):
+    """No page is left: the write that follows (every layer's) must not land on the rows' older tokens, which other
+    rows may share."""
+    pages, k, v, new = _full_pool()
+    k0, v0 = k.clone(), v.clone()
+    both = _i32([0, 1])
+    kn, vn = new(2, 1)
+    kdn.pages_reserve(pages, both, counts if isinstance(counts, int) else _i32(counts))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_CAPACITY
+    for _ in range(2):
+        kdn.pages_write(pages, both, kn, vn, k, v, counts=None if isinstance(counts, int) else _i32(counts))
+        assert torch.equal(k, k0) and torch.equal(v, v0)
+    # row 2 was not in the refused call: its own tokens may still be written
+    kn2, vn2 = new(1, 16)
+    kdn.pages_write(pages, _i32([2]), kn2, vn2, k, v)
+    assert _rows_hold(pages, k, v, 2, kn2[0], vn2[0])
+    # other books' calls between the refusal and the write do not lift it
+    kdn.pages_compact(pages)
+    kdn.pages_free(pages, _i32([3]))
+    k0, v0 = k.clone(), v.clone()
+    kdn.pages_write(pages, both, kn, vn, k, v)
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+    # a page is there again: the reservation and its write go through
+    kdn.pages_free(pages, _i32([2]))
+    kdn.pages_reserve(pages, both, 1)
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK
+    kdn.pages_write(pages, both, kn, vn, k, v)
+    assert _rows_hold(pages, k, v, 0, kn[0], vn[0]) and _rows_hold(pages, k, v, 1, kn[1], vn[1])
+
+
+@pytest.mark.parametrize("rows,counts", [([0, 1, 0], [1, 1, 1]), ([0, 1, 9], [1, 1, 1]), ([1, 0, -1], [1, 1, 1]),
+                                         ([0, 1, 3], [1, 1, 25]), ([0, 1, 3], [1, -1, 1])])
+def test_every_kind_of_refusal_holds_the_write_back(rows, counts):
+    """Rows listed twice or out of range, a row too long for the table, a negative count."""
+    pages, k, v, new = _full_pool()
+    kdn.pages_free(pages, _i32([2]))
+    k0, v0 = k.clone(), v.clone()
+    kdn.pages_reserve(pages, _i32(rows), _i32(counts))
+    assert kdn.read_device_status(pages.workspace) != kdn.KDN_OK
+    kdn.pages_write(pages, _i32(rows), *new(3, 1), k, v)
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+    kn, vn = new(1, 3)  # adding no token is a reservation too: the newest tokens may be written again
+    kdn.pages_reserve(pages, _i32([1]), 0)
+    kdn.pages_write(pages, _i32([1]), kn, vn, k, v)
+    assert _rows_hold(pages, k, v, 1, kn[0], vn[0])
+
+
+def test_a_row_that_is_emptied_or_forked_anew_forgets_its_refusal():
+    pages, k, v, new = _full_pool()
+    kdn.pages_reserve(pages, _i32([0, 1]), 1)  # refused
+    kdn.pages_free(pages, _i32([1]))
+    kdn.pages_copy(kdn.pages_fork(pages, _i32([0]), _i32([1])), k, v)
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK
+    kn, vn = new(2, 1)
+    before = k.clone()
+    kdn.pages_write(pages, _i32([0]), kn[:1], vn[:1], k, v)  # row 0 itself: still held back
+    assert torch.equal(k, before)
+    kdn.pages_write(pages, _i32([1]), kn[1:], vn[1:], k, v)  # asks for the newest token of the copy
+    assert _rows_hold(pages, k, v, 1, kn[1], vn[1])
+
+
+def test_a_captured_reservation_and_write_follow_the_pool():
+    """One graph of a reservation and its write, replayed while no page is left and again when there is one."""
+    pages, k, v, new = _full_pool()
+    both = _i32([0, 1])
+    kn, vn = new(2, 1)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        kdn.pages_reserve(pages, both, 1)
+        kdn.pages_write(pages, both, kn, vn, k, v)
+    k0 = k.clone()
+    graph.replay()
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_CAPACITY and torch.equal(k, k0)
+    kdn.pages_free(pages, _i32([2]))
+    for n in (9, 10, 11):
+        for x in (kn, vn):
+            x.add_(1)
+        graph.replay()
+        assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK and pages.lens.tolist()[:2] == [n, n]
+        assert _rows_hold(pages, k, v, 0, kn[0], vn[0]) and _rows_hold(pages, k, v, 1, kn[1], vn[1])
+
+
+def test_books_that_no_call_has_touched_report_no_error():
+    """The status word of new books, whatever the memory they got held before."""
+    for _ in range(20):
+        torch.full((1 << 14,), -1, dtype=torch.int32, device=DEV)  # freed at once: the next small arrays may lie here
+        pages = kdn.make_pages(64, 16, 8, 4)
+        assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK
+        torch.full((1 << 8,), -1, dtype=torch.int32, device=DEV)
+        assert kdn.read_device_status(kdn.Pages(pages.table, pages.lens, pages.refs, 16).workspace) == kdn.KDN_OK
+        del pages
