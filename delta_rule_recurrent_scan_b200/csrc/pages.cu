@@ -67,9 +67,16 @@ __device__ __forceinline__ bool mark(Shared& s, int r) {  // false: it was marke
   const unsigned bit = 1u << (r & 31);
   return (atomicOr(&s.seen[r >> 5], bit) & bit) == 0;
 }
+__device__ __forceinline__ bool unmark(Shared& s, int r) {  // whether it was marked
+  const unsigned bit = 1u << (r & 31);
+  return (atomicAnd(&s.seen[r >> 5], ~bit) & bit) != 0;
+}
 __device__ __forceinline__ bool marked(const Shared& s, int r) { return (s.seen[r >> 5] >> (r & 31)) & 1u; }
 
 __device__ __forceinline__ int pages_of(const PagesArgs& p, int len) { return (len + p.page_size - 1) / p.page_size; }
+
+__device__ __forceinline__ bool in_pool(const PagesArgs& p, int page) { return page >= 0 && page < p.num_pages; }
+__device__ __forceinline__ bool in_use(const PagesArgs& p, int page) { return in_pool(p, page) && p.refs[page] > 0; }
 
 // The ``want`` lowest free pages into p.scratch, rising; false when there are fewer.
 __device__ bool find_free(const PagesArgs& p, Shared& s, int want) {
@@ -159,14 +166,24 @@ __global__ void __launch_bounds__(kBook, 1) pages_fork_kernel(PagesArgs p, int n
     if (a < 0 || a >= p.rows || b < 0 || b >= p.rows) { bad |= kStatusInvalid; continue; }
     if (p.lens[a] < 0 || p.lens[a] > most || p.lens[b] != 0 || !mark(s, b)) bad |= kStatusInvalid;
   }
+  if (bad) atomicOr(&s.bad, bad);
   __syncthreads();
+  const bool rows_fine = s.bad == 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
   int need = 0;
-  if (!bad)
+  if (rows_fine) {
     for (int i = threadIdx.x; i < n; i += kBook) {
       if (marked(s, src[i])) bad |= kStatusInvalid;  // a row that is written by this call
       need += p.lens[src[i]] % p.page_size != 0;
     }
-  if (bad) atomicOr(&s.bad, bad);
+    for (int i = threadIdx.x >> 5; i < n; i += kBook / 32) {  // one warp per row: every entry names a page in use
+      const int held = pages_of(p, p.lens[src[i]]);
+      for (int e = lane; e < held; e += 32)
+        if (!in_use(p, p.table[(size_t)src[i] * p.max_pages + e])) bad |= kStatusInvalid;
+    }
+    if (bad) atomicOr(&s.bad, bad);
+  }
   int total;
   scan_cta(s, need, total);
   if (s.bad == 0 && total > 0 && !find_free(p, s, total)) {
@@ -195,58 +212,65 @@ __global__ void __launch_bounds__(kBook, 1) pages_fork_kernel(PagesArgs p, int n
         const int full = len / p.page_size, old = p.table[(size_t)src[i] * p.max_pages + full], page = p.scratch[at];
         p.table[(size_t)dst[i] * p.max_pages + full] = page;
         p.refs[page] = 1;
-        if (old >= 0 && old < p.num_pages) mv = make_int2(old, page);
-        else atomicOr(&s.bad, kStatusInvalid);
+        mv = make_int2(old, page);
       }
       moves[i] = mv;
       p.lens[dst[i]] = len, p.refused[dst[i]] = 0;
     }
   }
   // the full pages are shared: one warp per row
-  const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < n; i += kBook / 32) {
     const int full = p.lens[src[i]] / p.page_size;
     for (int e = lane; e < full; e += 32) {
       const int page = p.table[(size_t)src[i] * p.max_pages + e];
       p.table[(size_t)dst[i] * p.max_pages + e] = page;
-      if (page >= 0 && page < p.num_pages) atomicAdd(&p.refs[page], 1);
-      else atomicOr(&s.bad, kStatusInvalid);
+      atomicAdd(&p.refs[page], 1);
     }
   }
-  __syncthreads();
-  if (threadIdx.x == 0) *p.status = s.bad;
+  if (threadIdx.x == 0) *p.status = 0;
 }
 
+// Counts down first: when an entry names no page, or a page more often than it was counted, the counts are put back and
+// nothing else has changed.  One warp per row; a row listed twice is the warp's that marks (then unmarks) it first.
 __global__ void __launch_bounds__(kBook, 1) pages_free_kernel(PagesArgs p, int n, const int* rows) {
-  __shared__ unsigned bad_s;
-  if (threadIdx.x == 0) bad_s = 0;
+  __shared__ Shared s;
+  clear_rows(s, p.rows);
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kBook)
-    if (rows[i] < 0 || rows[i] >= p.rows || p.lens[rows[i]] < 0) atomicOr(&bad_s, kStatusInvalid);
-  __syncthreads();
-  if (bad_s == 0) {
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < n; i += kBook / 32) {
-      const int r = rows[i];
-      int len = 0;
-      if (lane == 0) len = atomicExch(&p.lens[r], 0), p.refused[r] = 0;  // a row listed twice is freed once
-      len = __shfl_sync(0xffffffffu, len, 0);
-      const int held = min(pages_of(p, min(len, 0x7fffffff - p.page_size)), p.max_pages);
-      for (int e = lane; e < held; e += 32) {
-        int& entry = p.table[(size_t)r * p.max_pages + e];
-        const int page = entry;
-        entry = -1;
-        if (page < 0 || page >= p.num_pages) {
-          atomicOr(&bad_s, kStatusInvalid);
-        } else if (atomicSub(&p.refs[page], 1) <= 0) {  // it was free already: not below zero
-          atomicAdd(&p.refs[page], 1);
-          atomicOr(&bad_s, kStatusInvalid);
-        }
-      }
-    }
+  const long long most = (long long)p.max_pages * p.page_size;
+  for (int i = threadIdx.x; i < n; i += kBook) {
+    const int r = rows[i];
+    if (r < 0 || r >= p.rows || p.lens[r] < 0 || p.lens[r] > most) atomicOr(&s.bad, kStatusInvalid);
   }
   __syncthreads();
-  if (threadIdx.x == 0) *p.status = bad_s;
+  const bool rows_fine = s.bad == 0;
+  __syncthreads();
+  if (rows_fine) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = warp; i < n; i += kBook / 32) {
+      const int r = rows[i];
+      if (!__shfl_sync(0xffffffffu, lane == 0 && mark(s, r), 0)) continue;
+      const int held = pages_of(p, p.lens[r]);
+      for (int e = lane; e < held; e += 32) {
+        const int page = p.table[(size_t)r * p.max_pages + e];
+        if (!in_pool(p, page) || atomicSub(&p.refs[page], 1) <= 0) atomicOr(&s.bad, kStatusInvalid);
+      }
+    }
+    __syncthreads();
+    const bool fine = s.bad == 0;
+    for (int i = warp; i < n; i += kBook / 32) {
+      const int r = rows[i];
+      if (!__shfl_sync(0xffffffffu, lane == 0 && unmark(s, r), 0)) continue;
+      const int held = pages_of(p, p.lens[r]);
+      for (int e = lane; e < held; e += 32) {
+        int& entry = p.table[(size_t)r * p.max_pages + e];
+        if (fine) entry = -1;
+        else if (in_pool(p, entry)) atomicAdd(&p.refs[entry], 1);
+      }
+      __syncwarp();
+      if (fine && lane == 0) p.lens[r] = 0, p.refused[r] = 0;
+    }
+  }
+  if (threadIdx.x == 0) *p.status = s.bad;
 }
 
 // The i-th used page behind the first U (U = number of used pages) goes into the i-th free page before it.

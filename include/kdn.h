@@ -343,7 +343,8 @@ typedef struct kdn_pages {
 } kdn_pages;
 
 /* Book-keeping calls.  Each is carried out as a whole or, when it cannot be, changes nothing and sets the status
- * word (kdn_read_device_status): KDN_ERR_INVALID_ARG for a row out of range or listed twice, KDN_ERR_CAPACITY
+ * word (kdn_read_device_status): KDN_ERR_INVALID_ARG for a row out of range or listed twice, for books that do not agree
+ * (a length outside the table, a forked or freed row's entry that names no page in use), KDN_ERR_CAPACITY
  * when no page or no table entry is left.  New pages are the lowest free ones, in the order of the list.  rows
  * are device arrays of n int32.  workspace: kdn_pages_workspace_bytes(pages) bytes, one for all calls on a cache and set
  * to zero once with its books; asynchronous; the calls on one cache must be ordered (one stream, or events).

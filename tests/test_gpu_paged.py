@@ -574,3 +574,52 @@ def test_books_that_no_call_has_touched_report_no_error():
         torch.full((1 << 8,), -1, dtype=torch.int32, device=DEV)
         assert kdn.read_device_status(kdn.Pages(pages.table, pages.lens, pages.refs, 16).workspace) == kdn.KDN_OK
         del pages
+
+
+def _books(pages):
+    return [pages.table.clone(), pages.lens.clone(), pages.refs.clone()]
+
+
+@pytest.mark.parametrize("entry", [-1, 40, 2**31 - 1, -(2**31), "free"])
+@pytest.mark.parametrize("at", [0, 2, 3])
+def test_calls_that_meet_a_broken_entry_change_nothing(entry, at):
+    """Row 2 (3 full pages and a part of one) has an entry that names no page, or one that is free: fork and free refuse
+    the whole call, other rows' parts of it too."""
+    pages = kdn.make_pages(40, 4, 8, 6)
+    kdn.pages_reserve(pages, _i32([0, 2, 4]), _i32([9, 14, 8]))
+    pages.table[2, at] = entry if entry != "free" else 39
+    before = _books(pages)
+    moves = kdn.pages_fork(pages, _i32([0, 2, 4]), _i32([1, 3, 5]))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_INVALID_ARG
+    assert bool((moves == -1).all()) and all(torch.equal(a, b) for a, b in zip(before, _books(pages)))
+    kdn.pages_free(pages, _i32([0, 2, 2, 4]))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(before, _books(pages)))
+    # without that row both go through
+    kdn.pages_fork(pages, _i32([0, 4]), _i32([1, 5]))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK
+    kdn.pages_free(pages, _i32([0, 4, 0, 1, 5]))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK
+    assert pages.lens.tolist() == [0, 0, 14, 0, 0, 0, 0, 0]
+    held = [p for p in pages.table[2].tolist() if 0 <= p < 40 and p != 39]
+    assert int(pages.refs.sum()) == 4 and all(int(pages.refs[p]) == 1 for p in held)
+
+
+def test_free_refuses_counts_and_lengths_that_do_not_agree():
+    """Two rows that name a page counted once, and a row longer than the table: nothing changes."""
+    pages = kdn.make_pages(40, 4, 8, 6)
+    kdn.pages_reserve(pages, _i32([0, 1, 2]), _i32([9, 14, 8]))
+    pages.table[1, 1] = pages.table[0, 2]
+    before = _books(pages)
+    kdn.pages_free(pages, _i32([2, 0, 1]))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(before, _books(pages)))
+    kdn.pages_free(pages, _i32([0, 2]))
+    assert kdn.read_device_status(pages.workspace) == kdn.KDN_OK
+    pages.lens[4] = 25
+    before = _books(pages)
+    for call in (lambda: kdn.pages_free(pages, _i32([4])), lambda: kdn.pages_fork(pages, _i32([4]), _i32([5])),
+                 lambda: kdn.pages_reserve(pages, _i32([4]), 0)):
+        call()
+        assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_INVALID_ARG
+        assert all(torch.equal(a, b) for a, b in zip(before, _books(pages)))
