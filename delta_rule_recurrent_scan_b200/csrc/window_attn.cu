@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(total<DK, DV, R>(kDqRest
     lse[i] = in ? p.lse[qrow + t_w + i] * kLog2e : 0.f;
     delta[i] = in ? p.delta[qrow + t_w + i] : 0.f;
   }
-  const int n = kt.count(), before = window::exact_delta<kT>(p, kt, t0) ? n : 0;
+  const int n = kt.count(), before = window::exact_delta<kT>(p, kt, t0, p.out_dtype == kBF16) ? n : 0;
   float sum[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) sum[i] = 0.f;

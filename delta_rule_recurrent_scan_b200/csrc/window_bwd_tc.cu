@@ -13,7 +13,8 @@
 //   queries: S and dP have the query on the lane; dq += dS k.  S is free as soon as it is in registers, so the next
 //            tile's S and dP (two buffers) run while this tile's dS is made.
 //
-// P and dS are rounded to bf16 for their product (the other operand's type; 2^-8 of a weight at most); the sums are fp32.
+// P and dS are rounded to bf16 for their product (the other operand's type; 2^-8 of a weight at most), and so is a dO that
+// comes as fp32; the sums are fp32.
 // A warpgroup takes half of a tile's columns: thread = (lane, half).  One load warp (TMA rings), one warp whose first
 // lane issues the products.  Rows behind a sequence's end are zeroed in shared memory.
 //
@@ -74,6 +75,10 @@ __global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* 
         g[i] = c.x, g[i + 1] = c.y, g[i + 2] = c.z, g[i + 3] = c.w;
       }
       *reinterpret_cast<uint4*>(dO16 + at) = pack8_bf16(g, 1.f);  // an operand of two bf16 products
+      // delta from the same dO as dP: with the unrounded one P (dP - delta) would not add up to zero along a row (2.5 to
+      // 3.1 times the error of a rounded gradient where rows see few keys, 1.8 where they see many; 1.7 this way)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = __bfloat162float(__float2bfloat16_rn(g[i]));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) x = fmaf(o[i], g[i], x);
@@ -399,7 +404,7 @@ __device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const Query
   w.len = window::seq_len(p, b);
   w.kt = window::key_tiles<kT>(w.t0, min(w.t0 + kT, w.len) - 1, p.window, p.n_sink);
   w.n = w.t0 < w.len ? w.kt.count() : 0;
-  w.before = window::exact_delta<kT>(p, w.kt, w.t0) ? w.n : 0;
+  w.before = window::exact_delta<kT>(p, w.kt, w.t0, true) ? w.n : 0;
   return w;
 }
 // The r-th work of this CTA: every other round runs backwards, so that long and short works meet.

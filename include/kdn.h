@@ -313,8 +313,9 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  * delta_t = dO_t . o_t, P_tj = exp(scale q_t . k_j - lse_t) and dS_tj = P_tj (dO_t . v_j - delta_t):
  *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
  * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
- * gradients do not change from run to run.  Where rows see few keys and o is bf16, delta is made from P and dP
- * instead of the rounded o.  Rows behind a sequence's last token are left as they were or set to zero (zero_rest),
+ * gradients do not change from run to run.  On the tensor cores P and dS enter their products as bf16, and so does
+ * dO, which is rounded to bf16 first where it comes as fp32.  Where rows see few keys and o is bf16 or comes from the
+ * tensor cores, delta is made from P and dP instead of o.  Rows behind a sequence's last token are left as they were or set to zero (zero_rest),
  * in all three; lse has no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink,
  * 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,

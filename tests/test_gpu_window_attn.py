@@ -336,3 +336,22 @@ def test_offsets_beyond_32_bits(dtype, d, backward):
         g = kdn.window_attn_backward(q, k, v, o, lse, dO, 70)
         g1 = kdn.window_attn_backward(q1, k, v, o1, lse1, dO1, 70)
         assert torch.equal(g["dq"][:, -1:], g1["dq"]) and torch.equal(g["dk"], g1["dk"]) and torch.equal(g["dv"], g1["dv"])
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("L,window,n_sink", [(40, 1000, 0), (500, 2, 0), (500, 3, 0), (500, 12, 4), (700, 200, 0), (900, 900, 0)])
+def test_gradient_error_with_fp32_outputs(L, window, n_sink, d):
+    """As test_gradient_error_where_rows_see_few_keys, for bf16 q, k, v with o and dO in fp32.  On the tensor cores dO is
+    rounded to bf16 for its products: a third rounding next to those of dS and of the result, as large and independent of
+    them: sqrt(3) in all.  That holds for a delta made from the same rounded dO (and, where rows see few keys, from the
+    unrounded weights); the fp32 path (d = 32) has the result's rounding only."""
+    q, k, v, dO = _inputs(2, 4, 2, L, d, d, torch.bfloat16, seed=23)
+    dO = torch.randn(dO.shape, generator=torch.Generator(device=DEV).manual_seed(24), device=DEV)
+    o, lse = kdn.window_attn(q, k, v, window, n_sink=n_sink, out_dtype=torch.float32)
+    g = kdn.window_attn_backward(q, k, v, o, lse, dO, window, n_sink=n_sink)
+    ref = dense(q, k, v, window, n_sink, dO=dO)
+    for name in ("dq", "dk"):
+        exact = ref[name][0]
+        off = float((g[name].double() - exact).norm())
+        rounded = float((exact.bfloat16().double() - exact).norm())
+        assert off <= ((3.0 if d >= 64 else 1.0) ** 0.5 + 0.1) * rounded, (name, off / rounded)
