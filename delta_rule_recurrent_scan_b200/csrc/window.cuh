@@ -38,7 +38,7 @@ __host__ __device__ __forceinline__ bool visible(int t, int j, int window, int n
 }
 
 // Tokens of sequence b: lens[b] held to [0, L], or L.
-__device__ __forceinline__ int seq_len(const WindowArgs& p, int b) {
+__host__ __device__ __forceinline__ int seq_len(const WindowArgs& p, int b) {
   if (p.lens == nullptr) return p.L;
   return min(max(p.lens[b], 0), p.L);
 }

@@ -68,8 +68,18 @@ struct Schedule {
   Divisor group, kv_heads, batch;
 };
 
+inline Schedule make_schedule(int B, int H, int Hkv, int L) {
+  const int G = H / Hkv, tiles = (L + kT - 1) / kT;
+  Schedule sch;
+  sch.heads = G % 2 == 0;
+  sch.tile_groups = sch.heads ? tiles : (tiles + 1) / 2;
+  sch.group = make_divisor(sch.heads ? G / 2 : G), sch.kv_heads = make_divisor(Hkv), sch.batch = make_divisor(B);
+  sch.works = (unsigned)((long long)B * Hkv * sch.tile_groups * sch.group.d);
+  return sch;
+}
+
 // n = 0: nothing to do.
-__device__ __forceinline__ Work make_work(const WindowArgs& p, const Schedule& sch, unsigned x) {
+__host__ __device__ __forceinline__ Work make_work(const WindowArgs& p, const Schedule& sch, unsigned x) {
   Work w;
   unsigned g, kvh, b;
   x = sch.group.div(x, g);
@@ -91,6 +101,22 @@ __device__ __forceinline__ Work make_work(const WindowArgs& p, const Schedule& s
   }
   w.n = w.qt[0] * kT < w.len ? w.ku.count() : 0;
   return w;
+}
+
+// After a wait of softmax group i's thread ``row`` gave up in round r: its rows of that work and of all later ones.
+template <int D>
+__host__ __device__ void mark_rest(const WindowArgs& p, const Schedule& sch, unsigned r, unsigned cta, unsigned ctas, int i, int row) {
+  const int width = D * (p.out_dtype == kBF16 ? 2 : 4);
+  for (; r * ctas < sch.works; ++r) {
+    const unsigned x = nth_work(r, cta, ctas);
+    if (x >= sch.works) continue;
+    const Work w = make_work(p, sch, x);
+    const int t = w.qt[i] * kT + row;
+    if (t >= p.L || (t >= w.len && !p.zero_rest)) continue;
+    const size_t at = ((size_t)w.b * p.H + w.h[i]) * p.L + t;
+    fill_words(p.o, at * width, width, t < w.len ? nan_word(p.out_dtype) : 0u);
+    p.lse[at] = t < w.len ? NAN : 0.f;
+  }
 }
 
 template <int D>
@@ -138,7 +164,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++nk;
       };
       for (unsigned r = 0; r * gridDim.x < sch.works && fine; ++r) {
-        const unsigned x = r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const unsigned x = nth_work(r, blockIdx.x, gridDim.x);
         if (x >= sch.works) continue;
         const Work w = make_work(p, sch, x);
         if (w.n == 0) continue;
@@ -173,7 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t p_phase[2] = {0, 0};
       unsigned nq = 0, nk = 0, nv = 0;  // tiles taken so far
       for (unsigned r = 0; r * gridDim.x < sch.works && fine; ++r) {
-        const unsigned x = r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const unsigned x = nth_work(r, blockIdx.x, gridDim.x);
         if (x >= sch.works) continue;
         const Work w = make_work(p, sch, x);
         if (w.n == 0) continue;
@@ -240,9 +266,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t t_s = tmem + lanes + 128 * i, t_o = tmem + lanes + 256 + D * i;
     const float c = p.scale * kLog2e;
     uint32_t phase = 0, done_phase = 0;
-    for (unsigned r = 0; r * gridDim.x < sch.works && fine; ++r) {
-        const unsigned x = r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (x >= sch.works) continue;
+    unsigned r = 0;
+    for (; r * gridDim.x < sch.works; ++r) {
+      const unsigned x = nth_work(r, blockIdx.x, gridDim.x);
+      if (x >= sch.works) continue;
       const Work w = make_work(p, sch, x);
       const int t0 = (i == 0 ? w.qt[0] : w.qt[1]) * kT, t = t0 + row;
       const size_t head = (size_t)w.b * p.H + (i == 0 ? w.h[0] : w.h[1]);
@@ -331,10 +358,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         done_phase ^= 1;
         sm100::tc_fence_after();
       }
-      if (!fine) {
-        if (t < w.len) p.lse[at] = NAN;
-        break;
-      }
+      if (!fine) break;
       const bool wide = is_wide(p.o);
       const float inv = 1.f / l;
       if (t < w.len) p.lse[at] = (m + log2f(l)) * kLn2;
@@ -358,6 +382,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       sm100::tc_fence_before();  // O is read: the next work's first product follows this warp's next arrival
     }
+    if (!fine) mark_rest<D>(p, sch, r, blockIdx.x, gridDim.x, i, row);
   }
   if (!fine) raise_status(p.status, kStatusTimeout);
   sm100::tc_fence_before();
@@ -371,20 +396,14 @@ cudaError_t forward(const WindowArgs& p, cudaStream_t stream) {
   if (!make_bf16_tmap_rows(&tq, p.q, p.B * p.H, p.L, D, kT) || !make_bf16_tmap_rows(&tk, p.k, p.B * p.Hkv, p.L, D, kT) ||
       !make_bf16_tmap_rows(&tv, p.v, p.B * p.Hkv, p.L, D, kT))
     return cudaErrorInvalidValue;
-  const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT;
-  Schedule sch;
-  sch.heads = G % 2 == 0;
-  sch.tile_groups = sch.heads ? tiles : (tiles + 1) / 2;
-  sch.group = make_divisor(sch.heads ? G / 2 : G), sch.kv_heads = make_divisor(p.Hkv), sch.batch = make_divisor(p.B);
-  const long long works = (long long)p.B * p.Hkv * sch.tile_groups * sch.group.d;
-  sch.works = (unsigned)works;
+  const Schedule sch = make_schedule(p.B, p.H, p.Hkv, p.L);
   const int smem = Smem<D>::kTotal + 1024;
   const cudaError_t e = cudaFuncSetAttribute(window_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return cudaErrorInvalidDevice;
-  window_fwd_tc_kernel<D><<<(unsigned)(works < sms ? works : sms), kTcThreads, smem, stream>>>(tq, tk, tv, p, sch);
+  window_fwd_tc_kernel<D><<<(sch.works < (unsigned)sms ? sch.works : (unsigned)sms), kTcThreads, smem, stream>>>(tq, tk, tv, p, sch);
   return cudaGetLastError();
 }
 

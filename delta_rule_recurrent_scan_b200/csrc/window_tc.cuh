@@ -73,8 +73,12 @@ __device__ __forceinline__ bool is_wide(const void* p) { return (reinterpret_cas
 // Division by a number known at launch: q = floor(x / d) for x < 2^31 (multiply by ceil(2^(32 + s) / d), s = ceil(log2 d)).
 struct Divisor {
   unsigned d, mul, shift;
-  __device__ __forceinline__ unsigned div(unsigned x, unsigned& rest) const {
+  __host__ __device__ __forceinline__ unsigned div(unsigned x, unsigned& rest) const {
+#ifdef __CUDA_ARCH__
     const unsigned q = (__umulhi(x, mul) + x) >> shift;
+#else
+    const unsigned q = (static_cast<unsigned>((unsigned long long)x * mul >> 32) + x) >> shift;
+#endif
     rest = x - q * d;
     return q;
   }
@@ -84,6 +88,19 @@ inline Divisor make_divisor(unsigned d) {
   while ((1ull << v.shift) < d) ++v.shift;
   v.mul = static_cast<unsigned>((((1ull << v.shift) - d) << 32) / d + 1);
   return v;
+}
+
+// The r-th of a call's works for this CTA: every other round runs backwards, so that long and short works meet.
+__host__ __device__ __forceinline__ unsigned nth_work(unsigned r, unsigned cta, unsigned ctas) {
+  return r * ctas + (r & 1 ? ctas - 1 - cta : cta);
+}
+
+// What a warp leaves in the rows that it cannot make any more because a wait gave up: NaN.  (Behind a sequence's end: zero,
+// where the call asks for it.)  ``bytes`` from ``at`` on, both multiples of 4; NaN in either type is all ones but the sign.
+__host__ __device__ __forceinline__ uint32_t nan_word(int dtype) { return dtype == kBF16 ? 0x7fff7fffu : 0x7fffffffu; }
+__host__ __device__ __forceinline__ void fill_words(void* p, size_t at, int bytes, uint32_t word) {
+  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<char*>(p) + at);
+  for (int e = 0; e < bytes / 4; ++e) to[e] = word;
 }
 
 // A warp's wait: true when every lane saw the phase complete.

@@ -301,8 +301,8 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights
  * enter the second product as bf16; sums, maxima and both products' accumulators are fp32), everything else
- * on the fp32 cores.  workspace: 256 bytes for the status word, or NULL: none is kept (a bounded wait that gives
- * up also leaves NaN in its rows of lse).  Asynchronous. */
+ * on the fp32 cores.  workspace: 256 bytes for the status word, or NULL: none is kept.  A bounded wait that gives up
+ * (KDN_ERR_TIMEOUT) also leaves NaN in every row of o and lse that was not made because of it.  Asynchronous. */
 KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, const void* k, const void* v,
                            const int* lens, int zero_rest, int window, int n_sink, float scale, void* o, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);

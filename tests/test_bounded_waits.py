@@ -8,6 +8,8 @@ import subprocess
 
 import pytest
 
+from delta_rule_recurrent_scan_b200 import build
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "delta_rule_recurrent_scan_b200", "csrc")
 FILES = ["window_attn_tc.cu", "window_bwd_tc.cu", "window_tc.cuh"]
 
@@ -68,3 +70,33 @@ def test_mbarrier_waits_use_that_loop():
     assert text.count("mbarrier.try_wait") == 1 and text.count("mbar_try_wait(") == 2
     body = text[text.index("bool mbar_wait_bounded"):]
     assert "return wait_bounded(" in body[:body.index("}\n\n")]
+
+
+def _host_check(name, tmp_path):
+    """Compiles a check that includes a kernel's source and runs its host part (no GPU call is made)."""
+    exe = tmp_path / name
+    native = os.path.join(os.path.dirname(os.path.abspath(__file__)), "native")
+    subprocess.run([build._nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "--expt-relaxed-constexpr",
+                    "-I", CSRC, "-I", build.INCLUDE, os.path.join(native, name + ".cu"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+needs_nvcc = pytest.mark.skipif(shutil.which(build._nvcc()) is None, reason="nvcc not available")
+
+
+def _role_ends(kernel, call):
+    """In the kernel's source: after its work loop, a warp whose wait gave up makes this call."""
+    for f in FILES:
+        for k, body in _kernels(_code(f)):
+            if k == kernel:
+                return re.search(r"if \(!fine\)\s*\{?\s*" + call, body) is not None
+    raise AssertionError(kernel)
+
+
+@needs_nvcc
+def test_forward_marks_every_row_it_could_not_make(tmp_path):
+    """A CTA takes work after work; behind a wait that gave up, every row of the work at hand and of all later ones is
+    NaN in o and lse (zero behind a sequence's end where the call asks for it), and nothing else is touched."""
+    assert _role_ends("window_fwd_tc_kernel", r"mark_rest<D>\(")
+    _host_check("window_fwd_marks_check", tmp_path)
