@@ -70,7 +70,7 @@ __host__ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int windo
 // which one sees a single key: with its weight taken as 1 its delta is dP to the bit, and the gradient of a softmax over
 // one key the zero that it is.
 template <int T>
-__device__ __forceinline__ bool exact_delta(const WindowArgs& p, const KeyTiles& k, int t0, bool rounded) {
+__host__ __device__ __forceinline__ bool exact_delta(const WindowArgs& p, const KeyTiles& k, int t0, bool rounded) {
   return (rounded && (k.hi - k.lo) * T <= 256) || t0 == 0 || (p.window == 1 && p.n_sink == 0);
 }
 __device__ __forceinline__ bool sees_one_key(const WindowArgs& p, int t) { return t == 0 || (p.window == 1 && p.n_sink == 0); }
@@ -146,7 +146,7 @@ inline KeyPass key_pass(int B, int H, int Hkv, int L, int window, int n_sink, in
 }
 // Key tile and (sequence, k/v head) of CTA x: the sinks' tiles come first (theirs are the longest walks), then the others.
 // Returns into how many parts the tile is cut; the CTA has part ``part``, whose slot in KeyPass::part is x.
-__device__ __forceinline__ int key_tile_of(KeyPass& kp, int heads, int tiles, unsigned x, int& part) {
+__host__ __device__ __forceinline__ int key_tile_of(KeyPass& kp, int heads, int tiles, unsigned x, int& part) {
   const unsigned cut = (unsigned)heads * kp.sinks * kp.parts;
   if (x < cut) {
     part = x % kp.parts, x /= kp.parts;
@@ -160,7 +160,7 @@ __device__ __forceinline__ int key_tile_of(KeyPass& kp, int heads, int tiles, un
   return kp.others;
 }
 // The parts of a cut tile: how many, and the first one's slot.
-__device__ __forceinline__ int parts_of(const KeyPass& kp, int heads, int tiles, size_t head, int tile, size_t& slot) {
+__host__ __device__ __forceinline__ int parts_of(const KeyPass& kp, int heads, int tiles, size_t head, int tile, size_t& slot) {
   if (tile < kp.sinks) {
     slot = (head * kp.sinks + tile) * kp.parts;
     return kp.parts;

@@ -89,6 +89,18 @@ __global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* 
 }
 
 // ------------------------------------------------------------------------------------------ dk, dv
+// What a thread (half 0: dv, 1: dk; key) leaves where a wait gave up: NaN in its row of the gradient, or in its row of the
+// part's slot, which makes the joined row NaN.
+template <int D>
+__host__ __device__ void mark_key(const WindowArgs& p, const KeyPass& kp, int parts, unsigned slot, int len, int half, int key) {
+  const int j = kp.tile * kT + key;
+  if (parts > 1) {
+    fill_words(kp.part, (((size_t)slot * 2 + half) * kT + key) * D * 4, 4 * D, nan_word(kF32));
+  } else if (j < len) {
+    fill_words(half == 0 ? p.dv : p.dk, ((size_t)kp.head * p.L + j) * 2 * D, 2 * D, nan_word(kBF16));
+  }
+}
+
 struct DkdvState {          // behind the tiles in shared memory: with them it fills the 227 KB of a block
   float rows[2][2][kT];     // -lse log2(e), -delta
   uint64_t kv_full, q_full[kSlots], q_empty[kSlots], do_full[2], do_empty[2], rows_full[2], s_ready, p_ready, dp_ready, ds_ready, done;
@@ -107,10 +119,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t &kv_full = st.kv_full, &s_ready = st.s_ready, &p_ready = st.p_ready, &dp_ready = st.dp_ready, &ds_ready = st.ds_ready,
            &done = st.done;
   uint64_t *q_full = st.q_full, *q_empty = st.q_empty, *do_full = st.do_full, *do_empty = st.do_empty, *rows_full = st.rows_full;
-  if (sm100::smem_u32(sm) & 1023) {  // never seen; the tiles' layout wants it and there is no room to align them here
-    raise_status(p.status, kStatusTimeout);
-    return;
-  }
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.H / p.Hkv, tiles = (p.L + kT - 1) / kT, bh = p.B * p.Hkv;
@@ -124,6 +132,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     zero_tile(p.dv, row0, 2 * D, j0, len, p.L, tid, kTcThreads);
   }
   if (j0 >= len) return;
+  if (sm100::smem_u32(sm) & 1023) {  // never seen; the tiles' layout wants it and there is no room to align them here
+    raise_status(p.status, kStatusTimeout);
+    if (tid < 2 * kT) mark_key<D>(p, kp, parts, blockIdx.x, len, tid / kT, tid % kT);
+    return;
+  }
   int lo, hi;
   window::query_tiles<kT>(j0, min(j0 + kT, len) - 1, len, p.window, p.n_sink, lo, hi);
   const int per = hi - lo, all = per * G;  // (head of the group, query tile), query tiles fastest
@@ -350,6 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
       }
     }
+    if (!fine) mark_key<D>(p, kp, parts, blockIdx.x, len, half, key);
   }
   if (!fine) raise_status(p.status, kStatusTimeout);
   sm100::tc_fence_before();
@@ -388,12 +402,16 @@ struct QueryPass {
   int tiles;
   Divisor group, kv_heads, batch;
 };
+inline QueryPass query_pass(int B, int H, int Hkv, int L) {
+  const int tiles = (L + kT - 1) / kT;
+  return QueryPass{(unsigned)((long long)B * H * tiles), tiles, make_divisor(H / Hkv), make_divisor(Hkv), make_divisor(B)};
+}
 struct QueryWork {
   int b, kvh, qrow, t0, len, n;  // n = 0: nothing to do
   int before;                    // key tiles of a first sweep: 0 or n
   KeyTiles kt;
 };
-__device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const QueryPass& qp, unsigned x) {
+__host__ __device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const QueryPass& qp, unsigned x) {
   unsigned g, kvh, b;
   x = qp.group.div(x, g);
   x = qp.kv_heads.div(x, kvh);
@@ -407,9 +425,17 @@ __device__ __forceinline__ QueryWork query_work(const WindowArgs& p, const Query
   w.before = window::exact_delta<kT>(p, w.kt, w.t0, true) ? w.n : 0;
   return w;
 }
-// The r-th work of this CTA: every other round runs backwards, so that long and short works meet.
-__device__ __forceinline__ unsigned nth_work(unsigned r) {
-  return r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+// After a wait of a thread (half of the columns, row) gave up in round r: its part of that work's dq and of all later ones'.
+template <int D>
+__host__ __device__ void mark_queries(const WindowArgs& p, const QueryPass& qp, unsigned r, unsigned cta, unsigned ctas, int half, int row) {
+  for (; r * ctas < qp.works; ++r) {
+    const unsigned x = nth_work(r, cta, ctas);
+    if (x >= qp.works) continue;
+    const QueryWork w = query_work(p, qp, x);
+    const int t = w.t0 + row;
+    if (t >= p.L || (t >= w.len && !p.zero_rest)) continue;
+    fill_words(p.dq, ((size_t)w.qrow * p.L + t) * 2 * D + half * D, D, t < w.len ? nan_word(kBF16) : 0u);
+  }
 }
 
 // A work may take two sweeps over its key tiles, the first for delta_t = sum_j P_tj dP_tj in fp32, which also replaces the
@@ -456,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm100::prefetch_tmap(&tm_q), sm100::prefetch_tmap(&tm_do), sm100::prefetch_tmap(&tm_k), sm100::prefetch_tmap(&tm_v);
       unsigned nq = 0, nk = 0, nv = 0;  // copies issued so far
       for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
-        const unsigned x = nth_work(r);
+        const unsigned x = nth_work(r, blockIdx.x, gridDim.x);
         if (x >= qp.works) continue;
         const QueryWork w = query_work(p, qp, x);
         const int row = w.b * p.Hkv + w.kvh;
@@ -496,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t q_desc = rows_desc(sm100::smem_u32(sm + S::kFixed)), do_desc = rows_desc(sm100::smem_u32(sm + S::kFixed + S::kTile));
     unsigned c = 0, nq = 0;  // key tiles and works begun
     for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
-      const unsigned x = nth_work(r);
+      const unsigned x = nth_work(r, blockIdx.x, gridDim.x);
       if (x >= qp.works) continue;
       const QueryWork w = query_work(p, qp, x);
       if (w.n == 0) continue;
@@ -553,8 +579,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const float2 c2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
     const bool wide = is_wide(p.dq);
     unsigned c = 0, works = 0, sweeps = 0;
-    for (unsigned r = 0; r * gridDim.x < qp.works && fine; ++r) {
-      const unsigned x = nth_work(r);
+    unsigned r = 0;
+    for (; r * gridDim.x < qp.works; ++r) {
+      const unsigned x = nth_work(r, blockIdx.x, gridDim.x);
       if (x >= qp.works) continue;
       const QueryWork w = query_work(p, qp, x);
       if (p.zero_rest && w.t0 + kT > w.len) zero_tile(p.dq, (size_t)w.qrow * p.L, 2 * D, w.t0, w.len, p.L, tid, 256);
@@ -663,6 +690,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       sm100::tc_fence_before();  // dq is read: the next work's first product follows this warp's next arrival
     }
+    if (!fine) mark_queries<D>(p, qp, r, blockIdx.x, gridDim.x, half, tid & 127);
   }
   if (!fine) raise_status(p.status, kStatusTimeout);
   sm100::tc_fence_before();
@@ -717,9 +745,7 @@ cudaError_t backward(const WindowArgs& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long long keys = window::key_ctas(kp, bh, tiles);
   const int cut_tiles = window::cut_tiles(kp, tiles);
-  QueryPass qp;
-  qp.works = (unsigned)((long long)p.B * p.H * tiles), qp.tiles = tiles;
-  qp.group = make_divisor(p.H / p.Hkv), qp.kv_heads = make_divisor(p.Hkv), qp.batch = make_divisor(p.B);
+  const QueryPass qp = query_pass(p.B, p.H, p.Hkv, p.L);
   // the queries' pass first: it may replace the rows' delta
   const unsigned ctas = qp.works < (unsigned)sms ? qp.works : (unsigned)sms;
   window_dq_tc_kernel<D><<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, td, p, rows, qp);

@@ -316,7 +316,8 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  * gradients do not change from run to run.  On the tensor cores P and dS enter their products as bf16, and so does
  * dO, which is rounded to bf16 first where it comes as fp32.  Where rows see few keys and o is bf16 or comes from the
  * tensor cores, delta is made from P and dP instead of o.  Rows behind a sequence's last token are left as they were or set to zero (zero_rest),
- * in all three; lse has no upstream gradient.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink,
+ * in all three; lse has no upstream gradient.  A bounded wait that gives up (KDN_ERR_TIMEOUT) leaves NaN in every row of
+ * dq, dk and dv that was not made because of it.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink,
  * 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
                                     const void* v, const int* lens, int zero_rest, int window, int n_sink, float scale,

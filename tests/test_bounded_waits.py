@@ -76,7 +76,7 @@ def _host_check(name, tmp_path):
     """Compiles a check that includes a kernel's source and runs its host part (no GPU call is made)."""
     exe = tmp_path / name
     native = os.path.join(os.path.dirname(os.path.abspath(__file__)), "native")
-    subprocess.run([build._nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "--expt-relaxed-constexpr",
+    subprocess.run([build._nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "-O2", "--expt-relaxed-constexpr",
                     "-I", CSRC, "-I", build.INCLUDE, os.path.join(native, name + ".cu"), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
@@ -100,3 +100,11 @@ def test_forward_marks_every_row_it_could_not_make(tmp_path):
     NaN in o and lse (zero behind a sequence's end where the call asks for it), and nothing else is touched."""
     assert _role_ends("window_fwd_tc_kernel", r"mark_rest<D>\(")
     _host_check("window_fwd_marks_check", tmp_path)
+
+
+@needs_nvcc
+def test_backward_marks_every_row_it_could_not_make(tmp_path):
+    """dq: as the forward.  dk and dv: a CTA's key tile, or the slot of its part of a cut one, which the join then adds
+    up to NaN."""
+    assert _role_ends("window_dq_tc_kernel", r"mark_queries<D>\(") and _role_ends("window_dkdv_tc_kernel", r"mark_key<D>\(")
+    _host_check("window_bwd_marks_check", tmp_path)
