@@ -62,7 +62,7 @@ struct Span {
 kdn_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
   auto meet = [](const Span& a, const Span& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x != 0 && y != 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
+    return x != 0 && y != 0 && a.bytes != 0 && b.bytes != 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
   };
   for (const Span* a = outs.begin(); a != outs.end(); ++a) {
     for (const Span* b = a + 1; b != outs.end(); ++b)
@@ -74,6 +74,9 @@ kdn_status check_apart(std::initializer_list<Span> outs, std::initializer_list<S
 }
 
 size_t elem_bytes(kdn_dtype t) { return t == KDN_BF16 ? 2 : 4; }
+Span ints(const char* name, const void* p, long long n) { return {name, p, n > 0 ? (size_t)n * sizeof(int) : 0}; }
+Span table_of(const kdn_pages* p) { return {"table", p->table, (size_t)p->rows * p->max_pages * sizeof(int)}; }
+Span lens_of(const kdn_pages* p) { return ints("lens", p->lens, p->rows); }
 
 // ---------------------------------------------------------------------------------------- paged cache
 bool pages_sizes_ok(const kdn_pages* p) {
@@ -107,10 +110,12 @@ kdn::PagesArgs pages_args(const kdn_pages* p, void* ws) {
   return a;
 }
 
-// A book-keeping call's checks; switches to the table's device.
-kdn_status book_checks(const kdn_pages* p, int n, const void* ws, size_t ws_bytes, DeviceGuard& guard) {
+// A book-keeping call's checks; switches to the table's device.  list: the pairs that it writes; ins: the lists it reads.
+kdn_status book_checks(const kdn_pages* p, int n, const void* ws, size_t ws_bytes, const Span& list,
+                       std::initializer_list<Span> ins, DeviceGuard& guard) {
   KDN_TRY(check_pages(p));
   if (n < 0) return fail(KDN_ERR_INVALID_ARG, "n must be >= 0");
+  KDN_TRY(check_apart({table_of(p), lens_of(p), ints("refs", p->refs, p->num_pages), {"workspace", ws, ws_bytes}, list}, ins));
   KDN_TRY(check_ptr(p->table, "table", 4, false));
   KDN_TRY(check_ptr(p->lens, "lens", 4, false));
   KDN_TRY(check_ptr(p->refs, "refs", 4, false));
@@ -134,11 +139,17 @@ kdn_status check_pool(int kv_heads, int dk, int dv, kdn_dtype dtype) {
 // workspace: of the books, or NULL to write whatever the last reservations came to.
 kdn_status write_pages(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens, int kv_heads, int dk,
                        int dv, kdn_dtype dtype, const void* k_new, const void* v_new, void* k_pages, void* v_pages,
-                       void* workspace, void* stream) {
+                       void* workspace, size_t workspace_bytes, void* stream) {
   KDN_TRY(check_pages(pages));
   if (n < 0 || tokens < 0) return fail(KDN_ERR_INVALID_ARG, "n and tokens must be >= 0");
   if (tokens > 1 << 24) return fail(KDN_ERR_UNSUPPORTED, "tokens must be at most 2^24");
   KDN_TRY(check_pool(kv_heads, dk, dv, dtype));
+  const int es = (int)elem_bytes(dtype);
+  const size_t fresh = (size_t)n * kv_heads * tokens * es, pool = (size_t)pages->num_pages * kv_heads * pages->page_size * es;
+  KDN_TRY(check_apart({{"k_pages", k_pages, pool * dk}, {"v_pages", v_pages, pool * dv}},
+                      {{"k_new", k_new, fresh * dk}, {"v_new", v_new, fresh * dv}, table_of(pages), lens_of(pages),
+                       ints("rows", rows, n), ints("counts", counts, n),
+                       {"workspace", workspace, workspace_bytes}}));
   const bool none = n == 0 || tokens == 0;
   KDN_TRY(check_ptr(pages->table, "table", 4, false));
   KDN_TRY(check_ptr(pages->lens, "lens", 4, false));
@@ -148,10 +159,10 @@ kdn_status write_pages(const kdn_pages* pages, int n, const int* rows, const int
   KDN_TRY(check_ptr(v_new, "v_new", 16, none));
   KDN_TRY(check_ptr(k_pages, "k_pages", 16, false));
   KDN_TRY(check_ptr(v_pages, "v_pages", 16, false));
+  if (workspace != nullptr) KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_pages_workspace_bytes(pages)));
   if (none) return ok();
   DeviceGuard guard;
   KDN_TRY(use_device_of(k_pages, guard));
-  const int es = (int)elem_bytes(dtype);
   const kdn::PagesWrite w{n, kv_heads, tokens, dk * es, dv * es, rows, counts, k_new, v_new, k_pages, v_pages};
   return cuda_status(kdn::launch_pages_write(pages_args(pages, workspace), w, (cudaStream_t)stream), "page write launch");
 }
@@ -180,7 +191,7 @@ kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const void* q, co
   const Span q_{"q", q, rows * dims->dk * in}, k_{"k", k, keys * dims->dk * in}, v_{"v", v, keys * dims->dv * in};
   const Span o_{"o", o, rows * dims->dv * elem_bytes(dims->out_dtype)}, lse_{"lse", lse, rows * 4};
   const Span ws_{"workspace", workspace, workspace_bytes};
-  KDN_TRY(check_apart({o_, lse_, ws_}, {q_, k_, v_}));
+  KDN_TRY(check_apart({o_, lse_, ws_}, {q_, k_, v_, ints("lens", lens, dims->B)}));
   KDN_TRY(check_ptr(q, "q", 16, none));
   KDN_TRY(check_ptr(k, "k", 16, none));
   KDN_TRY(check_ptr(v, "v", 16, none));
@@ -213,7 +224,7 @@ kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const vo
   const Span o_{"o", o, rows * dims->dv * elem_bytes(dims->out_dtype)}, lse_{"lse", lse, rows * 4};
   const Span ws_{"workspace", workspace, workspace_bytes};
   const Span dO_{"dO", dO, o_.bytes}, dq_{"dq", dq, q_.bytes}, dk_{"dk", dk, k_.bytes}, dv_{"dv", dv, v_.bytes};
-  KDN_TRY(check_apart({dq_, dk_, dv_, ws_}, {q_, k_, v_, o_, lse_, dO_}));
+  KDN_TRY(check_apart({dq_, dk_, dv_, ws_}, {q_, k_, v_, o_, lse_, dO_, ints("lens", lens, dims->B)}));
   KDN_TRY(check_ptr(q, "q", 16, none));
   KDN_TRY(check_ptr(k, "k", 16, none));
   KDN_TRY(check_ptr(v, "v", 16, none));
@@ -249,7 +260,7 @@ kdn_status kdn_pages_reserve(const kdn_pages* pages, int n, const int* rows, con
                              void* workspace, size_t workspace_bytes, void* stream) {
   DeviceGuard guard;
   if (counts == nullptr && count < 0) return fail(KDN_ERR_INVALID_ARG, "count must be >= 0");
-  KDN_TRY(book_checks(pages, n, workspace, workspace_bytes, guard));
+  KDN_TRY(book_checks(pages, n, workspace, workspace_bytes, {"moves", nullptr, 0}, {ints("rows", rows, n), ints("counts", counts, n)}, guard));
   KDN_TRY(check_ptr(rows, "rows", 4, n == 0));
   KDN_TRY(check_ptr(counts, "counts", 4, true));
   return cuda_status(kdn::launch_pages_reserve(pages_args(pages, workspace), n, rows, counts, count, (cudaStream_t)stream),
@@ -259,7 +270,7 @@ kdn_status kdn_pages_reserve(const kdn_pages* pages, int n, const int* rows, con
 kdn_status kdn_pages_fork(const kdn_pages* pages, int n, const int* src_rows, const int* dst_rows, int* moves,
                           void* workspace, size_t workspace_bytes, void* stream) {
   DeviceGuard guard;
-  KDN_TRY(book_checks(pages, n, workspace, workspace_bytes, guard));
+  KDN_TRY(book_checks(pages, n, workspace, workspace_bytes, ints("moves", moves, 2LL * n), {ints("src_rows", src_rows, n), ints("dst_rows", dst_rows, n)}, guard));
   KDN_TRY(check_ptr(src_rows, "src_rows", 4, n == 0));
   KDN_TRY(check_ptr(dst_rows, "dst_rows", 4, n == 0));
   KDN_TRY(check_ptr(moves, "moves", 8, n == 0));
@@ -270,14 +281,14 @@ kdn_status kdn_pages_fork(const kdn_pages* pages, int n, const int* src_rows, co
 kdn_status kdn_pages_free(const kdn_pages* pages, int n, const int* rows, void* workspace, size_t workspace_bytes,
                           void* stream) {
   DeviceGuard guard;
-  KDN_TRY(book_checks(pages, n, workspace, workspace_bytes, guard));
+  KDN_TRY(book_checks(pages, n, workspace, workspace_bytes, {"moves", nullptr, 0}, {ints("rows", rows, n)}, guard));
   KDN_TRY(check_ptr(rows, "rows", 4, n == 0));
   return cuda_status(kdn::launch_pages_free(pages_args(pages, workspace), n, rows, (cudaStream_t)stream), "page free launch");
 }
 
 kdn_status kdn_pages_compact(const kdn_pages* pages, int* moves, void* workspace, size_t workspace_bytes, void* stream) {
   DeviceGuard guard;
-  KDN_TRY(book_checks(pages, 0, workspace, workspace_bytes, guard));
+  KDN_TRY(book_checks(pages, 0, workspace, workspace_bytes, ints("moves", moves, pages ? pages->num_pages / 2 * 2LL : 0), {}, guard));
   KDN_TRY(check_ptr(moves, "moves", 8, pages->num_pages < 2));
   return cuda_status(kdn::launch_pages_compact(pages_args(pages, workspace), moves, (cudaStream_t)stream),
                      "page compaction launch");
@@ -290,13 +301,15 @@ kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int page_size,
     return fail(KDN_ERR_UNSUPPORTED, "page_size must be a power of two up to 1024");
   KDN_TRY(check_pool(kv_heads, dk, dv, dtype));
   if ((long long)kv_heads * page_size * 128 * 4 > (1LL << 40)) return fail(KDN_ERR_UNSUPPORTED, "page too large");
+  const size_t head = (size_t)kv_heads * page_size * elem_bytes(dtype);
+  KDN_TRY(check_apart({{"k_pages", k_pages, num_pages * head * dk}, {"v_pages", v_pages, num_pages * head * dv}},
+                      {ints("moves", moves, 2LL * n)}));
   KDN_TRY(check_ptr(moves, "moves", 8, n == 0));
   KDN_TRY(check_ptr(k_pages, "k_pages", 16, false));
   KDN_TRY(check_ptr(v_pages, "v_pages", 16, false));
   if (n == 0) return ok();
   DeviceGuard guard;
   KDN_TRY(use_device_of(k_pages, guard));
-  const size_t head = (size_t)kv_heads * page_size * elem_bytes(dtype);
   return cuda_status(kdn::launch_pages_copy(moves, n, num_pages, head * dk, head * dv, k_pages, v_pages, (cudaStream_t)stream),
                      "page copy launch");
 }
@@ -304,17 +317,16 @@ kdn_status kdn_pages_copy(int n, const int* moves, int num_pages, int page_size,
 kdn_status kdn_pages_write(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens, int kv_heads,
                            int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new, void* k_pages,
                            void* v_pages, void* stream) {
-  return write_pages(pages, n, rows, counts, tokens, kv_heads, dk, dv, dtype, k_new, v_new, k_pages, v_pages, nullptr, stream);
+  return write_pages(pages, n, rows, counts, tokens, kv_heads, dk, dv, dtype, k_new, v_new, k_pages, v_pages, nullptr, 0, stream);
 }
 
 kdn_status kdn_pages_write_reserved(const kdn_pages* pages, int n, const int* rows, const int* counts, int tokens,
                                     int kv_heads, int dk, int dv, kdn_dtype dtype, const void* k_new, const void* v_new,
                                     void* k_pages, void* v_pages, const void* workspace, size_t workspace_bytes,
                                     void* stream) {
-  KDN_TRY(check_pages(pages));
-  KDN_TRY(check_workspace(workspace, workspace_bytes, kdn_pages_workspace_bytes(pages)));
+  if (workspace == nullptr) return fail(KDN_ERR_INVALID_ARG, "workspace is NULL");
   return write_pages(pages, n, rows, counts, tokens, kv_heads, dk, dv, dtype, k_new, v_new, k_pages, v_pages,
-                     const_cast<void*>(workspace), stream);
+                     const_cast<void*>(workspace), workspace_bytes, stream);
 }
 
 size_t kdn_paged_step_workspace_bytes(const kdn_pages* pages, int n, int H, int kv_heads, int dk, int dv,
@@ -343,7 +355,8 @@ kdn_status kdn_paged_attn_step(const kdn_pages* pages, int n, const int* rows, i
   if (rows == nullptr && n > pages->rows) return fail(KDN_ERR_INVALID_ARG, "n exceeds the table's rows");
   const size_t heads = (size_t)n * H, pool = (size_t)pages->num_pages * kv_heads * pages->page_size * elem_bytes(in_dtype);
   KDN_TRY(check_apart({{"o", o, heads * dv * elem_bytes(out_dtype)}, {"lse", lse, heads * 4}, {"workspace", workspace, workspace_bytes}},
-                      {{"q", q, heads * dk * elem_bytes(in_dtype)}, {"k_pages", k_pages, pool * dk}, {"v_pages", v_pages, pool * dv}}));
+                      {{"q", q, heads * dk * elem_bytes(in_dtype)}, {"k_pages", k_pages, pool * dk}, {"v_pages", v_pages, pool * dv},
+                       table_of(pages), lens_of(pages), ints("rows", rows, n)}));
   KDN_TRY(check_ptr(pages->table, "table", 4, false));
   KDN_TRY(check_ptr(pages->lens, "lens", 4, false));
   KDN_TRY(check_ptr(rows, "rows", 4, true));

@@ -296,7 +296,8 @@ KDN_EXPORT size_t kdn_hola_workspace_bytes(const kdn_dims* dims);
  * h / (H / kv_heads); kv_heads divides H.  lens [B] int32 or NULL (= L): tokens of each sequence, held to
  * [0, L]; what memory holds behind a sequence's last token takes no part (it may be NaN), and its rows of o
  * and lse are left as they were (zero_rest = 0) or set to zero (1).  window >= 1 (>= L: plain causal attention),
- * n_sink >= 0, 0 < scale <= 1e30.  Here and in the two calls below no output may overlap an input or another output.
+ * n_sink >= 0, 0 < scale <= 1e30.  Here and in all calls below (pages and books among them) no output may overlap an
+ * input or another output; that is checked.
  * The sequences' own tokens must be finite: a hidden token's weight is 0, and 0 times its value has to be 0.
  * Out: o [B,H,L,d_v] (dims->out_dtype), lse [B,H,L] fp32 (the backward needs it).  dims->chunk and
  * dims->segments are ignored.  bf16 with d_k = d_v in {64, 128} runs on the tensor cores (the softmax weights

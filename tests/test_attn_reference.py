@@ -209,3 +209,80 @@ def test_binding_refuses_numbers_beyond_32_bits():
     for bad in (dict(window=2**31), dict(window=4, n_sink=2**32 + 1)):
         with pytest.raises(ValueError, match="32 bits"):
             kdn.window_attn(x, x, x, **bad)
+
+
+def test_page_calls_refuse_arrays_that_overlap(L):
+    """kdn_pages_write, _write_reserved and _copy, the books' calls, and the integer arrays of the attention calls; from
+    the addresses alone."""
+    c = kdn.PagesC(num_pages=8, page_size=16, rows=4, max_pages=2, table=0x100000, lens=0x110000, refs=0x120000)
+    at = dict(k=0x200000, v=0x300000, kn=0x400000, vn=0x500000, rows=0x600000, counts=0x610000, moves=0x620000, ws=0x630000,
+              dst=0x640000)
+    ws = L.kdn_pages_workspace_bytes(ctypes.byref(c))
+
+    def call(name, *args):
+        st = getattr(L, name)(*args)
+        return st, L.kdn_last_error()
+
+    def write(**n):  # pages [8, 2, 16, 64] bf16: 32,768 bytes; new tokens [3, 2, 5, 64]: 3,840 bytes
+        a = {**at, **n}
+        return call("kdn_pages_write", ctypes.byref(c), 3, a["rows"], a["counts"], 5, 2, 64, 64, 1, a["kn"], a["vn"], a["k"],
+                    a["v"], None)
+
+    def reserved(**n):
+        a = {**at, **n}
+        return call("kdn_pages_write_reserved", ctypes.byref(c), 3, a["rows"], a["counts"], 5, 2, 64, 64, 1, a["kn"], a["vn"],
+                    a["k"], a["v"], a["ws"], ws, None)
+
+    def copy(**n):
+        a = {**at, **n}
+        return call("kdn_pages_copy", 3, a["moves"], 8, 16, 2, 64, 64, 1, a["k"], a["v"], None)
+
+    def reserve(**n):
+        a = {**at, **n}
+        return call("kdn_pages_reserve", ctypes.byref(c), 3, a["rows"], a["counts"], 0, a["ws"], ws, None)
+
+    def fork(**n):
+        a = {**at, **n}
+        return call("kdn_pages_fork", ctypes.byref(c), 3, a["rows"], a["dst"], a["moves"], a["ws"], ws, None)
+
+    def free(**n):
+        a = {**at, **n}
+        return call("kdn_pages_free", ctypes.byref(c), 3, a["rows"], a["ws"], ws, None)
+
+    def compact(**n):
+        a = {**at, **n}
+        return call("kdn_pages_compact", ctypes.byref(c), a["moves"], a["ws"], ws, None)
+
+    d = kdn.Dims(2, 4, 8, 64, 64, 0, 1, 1, 0)
+
+    def forward(lens):
+        return call("kdn_window_attn", ctypes.byref(d), 2, 0x10000, 0x20000, 0x30000, lens, 0, 4, 0, 1.0, 0x40000, 0x50000,
+                    None, 0, None)
+
+    def backward(lens):
+        return call("kdn_window_attn_backward", ctypes.byref(d), 2, 0x10000, 0x20000, 0x30000, lens, 0, 4, 0, 1.0, 0x40000,
+                    0x50000, 0x60000, 0x70000, 0x80000, 0x90000, 0xa0000, 256, None)
+
+    def step(o, rows=None):
+        return call("kdn_paged_attn_step", ctypes.byref(c), 2, rows, 4, 2, 64, 64, 1, 1, 0x10000, at["k"], at["v"], 0, 0, 1.0,
+                    o, None, None, 0, None)
+
+    for (st, said), says in (
+            (write(kn=at["k"] + 32752), b"k_pages overlaps k_new"), (write(vn=at["k"] + 16), b"k_pages overlaps v_new"),
+            (write(vn=at["v"] - 3824), b"v_pages overlaps v_new"), (write(k=at["v"] + 32752), b"k_pages overlaps v_pages"),
+            (write(rows=at["v"] + 64), b"v_pages overlaps rows"), (write(counts=at["k"]), b"k_pages overlaps counts"),
+            (write(k=0x110000), b"k_pages overlaps lens"), (write(v=0x100000 - 32752), b"v_pages overlaps table"),
+            (reserved(kn=at["k"] + 32752), b"k_pages overlaps k_new"), (reserved(ws=at["v"]), b"v_pages overlaps workspace"),
+            (copy(v=at["k"] + 32752), b"k_pages overlaps v_pages"), (copy(moves=at["v"] + 32760), b"v_pages overlaps moves"),
+            (reserve(rows=0x110004), b"lens overlaps rows"), (reserve(counts=0x100000), b"table overlaps counts"),
+            (reserve(ws=0x120000 - 256), b"refs overlaps workspace"), (reserve(rows=at["ws"] + 256), b"workspace overlaps rows"),
+            (fork(moves=0x11fff8), b"refs overlaps moves"), (fork(dst=at["moves"] + 16), b"moves overlaps dst_rows"),
+            (fork(rows=0x120000), b"refs overlaps src_rows"), (free(rows=0x100010), b"table overlaps rows"),
+            (compact(moves=0x110008), b"lens overlaps moves"),
+            (forward(0x40008), b"o overlaps lens"), (backward(0x70ffc - 0xffc), b"dq overlaps lens"),
+            (step(0x110000), b"o overlaps lens"), (step(0x100010), b"o overlaps table"), (step(0x10000 + 1024, 0x10000 + 1024), b"o overlaps rows")):
+        assert st == kdn.KDN_ERR_INVALID_ARG and said.endswith(says), (says, said)
+    for st, said in (write(kn=at["k"] + 32768), write(v=at["k"] + 32768), copy(v=at["k"] + 32768), copy(moves=at["v"] + 32768),
+                     reserve(rows=0x110010), fork(dst=at["moves"] + 24), fork(dst=at["rows"]), free(rows=0x100020),
+                     reserve(counts=at["rows"])):
+        assert b"overlaps" not in said, said  # neighbours, and lists that are only read
