@@ -63,15 +63,17 @@ __host__ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int windo
 
 // Whether the backward makes these queries' delta from the weights instead of from o, in a sweep of its own.  dO . o with o
 // rounded to bf16, or made from bf16 weights (``rounded``), is off by about 2^-9 |dO| |o|, the same for all keys of a row;
-// against P (dP - delta) that is
-// 1 / sqrt(n - 1) of what rounding dS costs for n keys of equal weight, so it shows where rows see few keys (the first
-// rows of every sequence hold a third of the gradient's energy: 1.5 times the error of the rounded result instead of
-// 1.4), and there the walk is short.  Up to 256 keys, in tiles of T; and, whatever o is, for queries from t0 on among
-// which one sees a single key: with its weight taken as 1 its delta is dP to the bit, and the gradient of a softmax over
-// one key the zero that it is.
+// against P (dP - delta) that is 1 / sqrt(n - 1) of what rounding dS costs for n keys of equal weight, so it shows where
+// rows see few keys (the first rows of every sequence hold a third of the gradient's energy: 1.5 times the error of the
+// rounded result instead of 1.4), and there the walk is short.  So: up to 256 keys of the window, in tiles of T, and no more
+// than 128 sinks before them (a row behind those sees them all; backward of 2 sequences of 4096, 16 heads on 4, d 128,
+// window 64, 2048 sinks: 464 us, 571 with sweeps over all the sinks' tiles).  And, whatever o is, for queries from t0 on among which
+// one sees a single key: with its weight taken as 1 its delta is dP to the bit, and the gradient of a softmax over one key
+// the zero that it is.
 template <int T>
 __host__ __device__ __forceinline__ bool exact_delta(const WindowArgs& p, const KeyTiles& k, int t0, bool rounded) {
-  return (rounded && (k.hi - k.lo) * T <= 256) || t0 == 0 || (p.window == 1 && p.n_sink == 0);
+  const bool few = (k.hi - k.lo) * T <= 256 && (k.sinks == 0 || p.n_sink <= 128);
+  return (rounded && few) || t0 == 0 || (p.window == 1 && p.n_sink == 0);
 }
 __device__ __forceinline__ bool sees_one_key(const WindowArgs& p, int t) { return t == 0 || (p.window == 1 && p.n_sink == 0); }
 

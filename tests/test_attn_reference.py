@@ -2,6 +2,9 @@
 refusals (no GPU)."""
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -286,3 +289,16 @@ def test_page_calls_refuse_arrays_that_overlap(L):
                      reserve(rows=0x110010), fork(dst=at["moves"] + 24), fork(dst=at["rows"]), free(rows=0x100020),
                      reserve(counts=at["rows"])):
         assert b"overlaps" not in said, said  # neighbours, and lists that are only read
+
+
+def test_first_sweeps_are_short(tmp_path):
+    """Which query tiles of the backward walk their keys twice (for delta from the weights): those whose rows see few keys,
+    sinks among them, and none whose walk is long.  The kernel's own code, compiled for the host."""
+    if shutil.which(build._nvcc()) is None:
+        pytest.skip("nvcc not available")
+    exe, here = tmp_path / "sweeps", os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([build._nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "-O2",
+                    "--expt-relaxed-constexpr", "-I", build.CSRC, "-I", build.INCLUDE,
+                    os.path.join(here, "native", "window_sweeps_check.cu"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-2000:] + r.stderr

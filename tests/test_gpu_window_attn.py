@@ -355,3 +355,20 @@ def test_gradient_error_with_fp32_outputs(L, window, n_sink, d):
         off = float((g[name].double() - exact).norm())
         rounded = float((exact.bfloat16().double() - exact).norm())
         assert off <= ((3.0 if d >= 64 else 1.0) ** 0.5 + 0.1) * rounded, (name, off / rounded)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("L,window,n_sink", [(1200, 64, 800), (1000, 3, 40), (900, 20, 130)])
+def test_gradient_error_of_small_windows_with_many_sinks(L, window, n_sink, out_dtype, d):
+    """The same bounds where the sinks, not the window, decide how many keys a row sees."""
+    q, k, v, dO = _inputs(2, 4, 2, L, d, d, torch.bfloat16, seed=25)
+    dO = dO.to(out_dtype)
+    o, lse = kdn.window_attn(q, k, v, window, n_sink=n_sink, out_dtype=out_dtype)
+    g = kdn.window_attn_backward(q, k, v, o, lse, dO, window, n_sink=n_sink)
+    ref = dense(q, k, v, window, n_sink, dO=dO)
+    for name in ("dq", "dk"):
+        exact = ref[name][0]
+        off = float((g[name].double() - exact).norm())
+        rounded = float((exact.bfloat16().double() - exact).norm())
+        assert off <= ((2.0 if d >= 64 else 1.0) ** 0.5 + 0.1) * rounded, (name, off / rounded)
