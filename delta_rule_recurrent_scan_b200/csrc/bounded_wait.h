@@ -8,10 +8,12 @@
 // CUDA include).
 #pragma once
 
+#ifndef KDN_HOST_DEVICE
 #ifdef __CUDACC__
 #define KDN_HOST_DEVICE __host__ __device__ __forceinline__
 #else
 #define KDN_HOST_DEVICE inline
+#endif
 #endif
 
 namespace kdn {

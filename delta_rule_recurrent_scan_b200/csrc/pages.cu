@@ -14,6 +14,7 @@
 // The data movers are bandwidth-bound copies of 16-byte words.
 #include "common.cuh"
 #include "kernels.h"
+#include "pages_need.h"
 
 namespace kdn {
 
@@ -27,7 +28,7 @@ struct Shared {
   unsigned seen[kMaxRows / 32];
   int warp_sum[33];
   unsigned bad;
-  unsigned long long need;
+  PageSum need;
 };
 
 // Exclusive prefix sum of x over the CTA; total gets the sum.
@@ -73,7 +74,7 @@ __device__ __forceinline__ bool unmark(Shared& s, int r) {  // whether it was ma
 }
 __device__ __forceinline__ bool marked(const Shared& s, int r) { return (s.seen[r >> 5] >> (r & 31)) & 1u; }
 
-__device__ __forceinline__ int pages_of(const PagesArgs& p, int len) { return (len + p.page_size - 1) / p.page_size; }
+__device__ __forceinline__ int pages_of(const PagesArgs& p, int len) { return kdn::pages_of(len, p.page_size); }
 
 __device__ __forceinline__ bool in_pool(const PagesArgs& p, int page) { return page >= 0 && page < p.num_pages; }
 __device__ __forceinline__ bool in_use(const PagesArgs& p, int page) { return in_pool(p, page) && p.refs[page] > 0; }
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kBook, 1) pages_reserve_kernel(PagesArgs p, in
   clear_rows(s, p.rows);
   __syncthreads();
   const long long most = (long long)p.max_pages * p.page_size;
-  long long need = 0;
+  PageSum need = 0;
   unsigned bad = 0;
   for (int i = threadIdx.x; i < n; i += kBook) {
     const int r = rows[i], c = counts ? counts[i] : count;
@@ -117,12 +118,12 @@ __global__ void __launch_bounds__(kBook, 1) pages_reserve_kernel(PagesArgs p, in
     const int len = p.lens[r];
     if (len < 0 || len > most || !mark(s, r)) { bad |= kStatusInvalid; continue; }
     if (len + (long long)c > most) { bad |= kStatusCapacity; continue; }
-    need += pages_of(p, len + c) - pages_of(p, len);
+    need += more_pages(len, c, p.page_size);
   }
   if (bad) atomicOr(&s.bad, bad);
-  if (need) atomicAdd(&s.need, (unsigned long long)need);
+  if (need) atomicAdd(&s.need, need);
   __syncthreads();
-  if (threadIdx.x == 0 && s.need > (unsigned long long)p.num_pages) atomicOr(&s.bad, kStatusCapacity);
+  if (threadIdx.x == 0 && pool_too_small(s.need, p.num_pages)) atomicOr(&s.bad, kStatusCapacity);
   __syncthreads();
   const int total = static_cast<int>(s.need);  // within num_pages where it is used
   if (s.bad == 0 && total > 0 && !find_free(p, s, total)) {

@@ -302,3 +302,17 @@ def test_first_sweeps_are_short(tmp_path):
                     os.path.join(here, "native", "window_sweeps_check.cu"), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout[-2000:] + r.stderr
+
+
+def test_needs_that_pass_32_bits_are_larger_than_any_pool(tmp_path):
+    """The sums behind kdn_pages_reserve, compiled for the host: no call on a GPU could show a sum that is too short
+    without handing out pages that are not there."""
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    exe, here = tmp_path / "need", os.path.dirname(os.path.abspath(__file__))
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", build.CSRC,
+                    os.path.join(here, "native", "pages_need_check.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+    kernel = open(os.path.join(build.CSRC, "pages.cu")).read()
+    assert "PageSum need;" in kernel and "PageSum need = 0;" in kernel and "pool_too_small(s.need" in kernel
