@@ -1,6 +1,7 @@
 // Host-only check of the sums behind a reservation (no GPU, no CUDA headers): needs that pass 31 and 32 bits are still
 // larger than any pool.  Exit status 0 when every check holds; the failing check is printed otherwise.
 #include <cstdio>
+#include <initializer_list>
 
 #include "pages_need.h"
 
