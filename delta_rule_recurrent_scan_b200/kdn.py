@@ -637,8 +637,8 @@ def window_attn_backward(q, k, v, o, lse, dO, window, n_sink=0, lens=None, scale
 class Pages:
     """The books of a paged cache (kdn_pages): table [rows, max_pages], lens [rows] and refs [num_pages], int32.  One
     set serves every layer; a layer's pages are k_pages [num_pages, kv_heads, page_size, d_k] and v_pages.
-    ``workspace`` (allocated with the books; one given here has to hold zeros) has the status of the last book-keeping
-    call, read_device_status(pages.workspace), and which rows' last reservation was refused."""
+    ``workspace`` (allocated with the books; one given here is set to zero) has the status of the last book-keeping call,
+    read_device_status(pages.workspace), and which rows' last reservation was refused."""
     table: torch.Tensor
     lens: torch.Tensor
     refs: torch.Tensor
@@ -646,13 +646,29 @@ class Pages:
     workspace: torch.Tensor | None = None
 
     def __post_init__(self):
-        self._own = None
-        if self.workspace is None and self.table.is_cuda:
+        self._own = self._home = None
+        self._fresh = True  # no call has come since the workspace was set to zero, on the stream _home
+        if self.workspace is not None:
+            if self.workspace.is_cuda:
+                self.workspace.zero_()
+                self._home = _stream_of(None, self.workspace.device)
+        elif self.table.is_cuda:
             self._allocate(self._c())
 
     def _allocate(self, c):
-        self.workspace = torch.zeros(max(256, lib().kdn_pages_workspace_bytes(c)), dtype=torch.uint8, device=self.table.device)
-        self._own = c.num_pages, c.rows
+        dev = self.table.device
+        self.workspace = torch.zeros(max(256, lib().kdn_pages_workspace_bytes(c)), dtype=torch.uint8, device=dev)
+        self._own, self._home, self._fresh = (c.num_pages, c.rows), _stream_of(None, dev), True
+
+    def _visit(self, stream, dev):
+        """A call on another stream than the workspace's own: the first one follows the zeros, and the memory stays the
+        workspace's until the call has ended.  (A capture begins behind all work.)"""
+        stream = torch.cuda.current_stream(dev) if stream is None else stream
+        with torch.cuda.stream(stream):
+            if self._fresh and self._home is not None and not torch.cuda.is_current_stream_capturing():
+                home = torch.cuda.ExternalStream(self._home, device=dev) if self._home else torch.cuda.default_stream(dev)
+                stream.wait_stream(home)
+        self.workspace.record_stream(stream)
 
     def _c(self, dev=None):
         table, lens, refs = self.table, self.lens, self.refs
@@ -679,18 +695,24 @@ def _list(t, name, dev):
     return _need(t, name, t.shape, torch.int32, dev)
 
 
-def _books(pages):
+def _books(pages, stream):
     c = pages._c()
+    dev = pages.table.device
     if pages._own not in (None, (c.num_pages, c.rows)):  # the books were exchanged for larger or smaller ones
-        pages._allocate(c)
-    return c, pages.table.device, pages.workspace
+        with _on(stream):
+            pages._allocate(c)
+    st = _stream_of(stream, dev)
+    if st != pages._home:
+        pages._visit(stream, dev)
+    pages._fresh = False
+    return c, dev, pages.workspace, st
 
 
 def pages_reserve(pages, rows, counts, stream=None):
     """Adds tokens to the listed rows (int32 [n]), with the pages they need: ``counts`` each, or counts[i] (int32 [n]).
     Refused as a whole where there is no room: read_device_status(pages.workspace) says so (it waits for the stream), and
     pages_write passes over the rows until a reservation succeeds."""
-    c, dev, ws = _books(pages)
+    c, dev, ws, at = _books(pages, stream)
     _list(rows, "rows", dev)
     each = isinstance(counts, torch.Tensor)
     if each:
@@ -698,7 +720,7 @@ def pages_reserve(pages, rows, counts, stream=None):
     else:
         _int32(counts, "counts")
     st = lib().kdn_pages_reserve(c, rows.numel(), _at(rows), _at(counts) if each else None,
-                                 0 if each else counts, _at(ws), ws.numel(), _stream_of(stream, dev))
+                                 0 if each else counts, _at(ws), ws.numel(), at)
     if st:
         _check(st, "kdn_pages_reserve")
 
@@ -706,7 +728,7 @@ def pages_reserve(pages, rows, counts, stream=None):
 def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
     """Makes each empty row dst_rows[i] a copy of src_rows[i], sharing its full pages.  Returns moves [n, 2] int32, the
     part-filled pages that pages_copy has to copy (in every layer) before the rows are used."""
-    c, dev, ws = _books(pages)
+    c, dev, ws, at = _books(pages, stream)
     _list(src_rows, "src_rows", dev)
     _need(dst_rows, "dst_rows", src_rows.shape, torch.int32, dev)
     with _on(stream):
@@ -714,7 +736,7 @@ def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
             moves = torch.empty(src_rows.numel(), 2, dtype=torch.int32, device=dev)
     _need(moves, "moves", (src_rows.numel(), 2), torch.int32, dev)
     st = lib().kdn_pages_fork(c, src_rows.numel(), _at(src_rows), _at(dst_rows), _at(moves), _at(ws),
-                              ws.numel(), _stream_of(stream, dev))
+                              ws.numel(), at)
     if st:
         _check(st, "kdn_pages_fork")
     return moves
@@ -722,9 +744,9 @@ def pages_fork(pages, src_rows, dst_rows, moves=None, stream=None):
 
 def pages_free(pages, rows, stream=None):
     """Empties the listed rows; pages that no row names any more are free."""
-    c, dev, ws = _books(pages)
+    c, dev, ws, at = _books(pages, stream)
     _list(rows, "rows", dev)
-    st = lib().kdn_pages_free(c, rows.numel(), _at(rows), _at(ws), ws.numel(), _stream_of(stream, dev))
+    st = lib().kdn_pages_free(c, rows.numel(), _at(rows), _at(ws), ws.numel(), at)
     if st:
         _check(st, "kdn_pages_free")
 
@@ -732,12 +754,12 @@ def pages_free(pages, rows, stream=None):
 def pages_compact(pages, moves=None, stream=None):
     """Moves the pages in use to the lowest page numbers.  Returns moves [num_pages // 2, 2] int32 for pages_copy (in
     every layer), ending in pairs of -1."""
-    c, dev, ws = _books(pages)
+    c, dev, ws, at = _books(pages, stream)
     with _on(stream):
         if moves is None:
             moves = torch.empty(c.num_pages // 2, 2, dtype=torch.int32, device=dev)
     _need(moves, "moves", (c.num_pages // 2, 2), torch.int32, dev)
-    st = lib().kdn_pages_compact(c, _at(moves), _at(ws), ws.numel(), _stream_of(stream, dev))
+    st = lib().kdn_pages_compact(c, _at(moves), _at(ws), ws.numel(), at)
     if st:
         _check(st, "kdn_pages_compact")
     return moves
@@ -774,7 +796,7 @@ def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream
     last reservation was refused are left as they are."""
     dev = pages.table.device
     num, Hkv, page, dk, dv = _pool(k_pages, v_pages, dev)
-    c, _, ws = _books(pages)
+    c, _, ws, at = _books(pages, stream)
     if num != c.num_pages or page != pages.page_size:
         raise ValueError(f"k_pages holds {num} pages of {page} tokens, the books {c.num_pages} of {pages.page_size}")
     _list(rows, "rows", dev)
@@ -787,7 +809,7 @@ def pages_write(pages, rows, k_new, v_new, k_pages, v_pages, counts=None, stream
     if counts is not None:
         _need(counts, "counts", (n,), torch.int32, dev)
     st = lib().kdn_pages_write_reserved(c, n, _at(rows), _at(counts), T, Hkv, dk, dv, _DTYPES[k_pages.dtype], _at(k_new),
-                                        _at(v_new), _at(k_pages), _at(v_pages), _at(ws), ws.numel(), _stream_of(stream, dev))
+                                        _at(v_new), _at(k_pages), _at(v_pages), _at(ws), ws.numel(), at)
     if st:
         _check(st, "kdn_pages_write_reserved")
 

@@ -316,3 +316,14 @@ def test_needs_that_pass_32_bits_are_larger_than_any_pool(tmp_path):
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
     kernel = open(os.path.join(build.CSRC, "pages.cu")).read()
     assert "PageSum need;" in kernel and "PageSum need = 0;" in kernel and "pool_too_small(s.need" in kernel
+
+
+def test_a_reserved_write_wants_the_books_workspace(L):
+    c = kdn.PagesC(num_pages=8, page_size=16, rows=4, max_pages=2)
+    args = [ctypes.byref(c), 1, None, None, 1, 2, 64, 64, 1, None, None, None, None]
+    assert L.kdn_pages_write_reserved(*args, None, 0, None) == kdn.KDN_ERR_INVALID_ARG
+    assert b"workspace" in L.kdn_last_error()
+    # a word per row beside the scratch of the searches
+    one = L.kdn_pages_workspace_bytes(ctypes.byref(c))
+    c.rows = 1 << 18
+    assert L.kdn_pages_workspace_bytes(ctypes.byref(c)) >= one - 256 + 4 * (1 << 18)

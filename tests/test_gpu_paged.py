@@ -623,3 +623,47 @@ def test_free_refuses_counts_and_lengths_that_do_not_agree():
         call()
         assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_INVALID_ARG
         assert all(torch.equal(a, b) for a, b in zip(before, _books(pages)))
+
+
+def test_a_first_call_on_another_stream_follows_the_making_of_the_books():
+    """The workspace is set to zero on the stream that is current when the books are made; a call on another stream, and
+    what it leaves in the workspace, must not be overtaken by that."""
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    table, lens, refs, rows = _i32([[-1] * 4] * 3), _i32([0] * 3), _i32([0] * 2), _i32([0, 1, 2])
+    kdn.pages_reserve(kdn.Pages(table, lens, refs, 4), rows, 0)  # a kernel's first launch may wait for the device
+    torch.cuda.synchronize()
+    for given in (False, True):
+        ws = torch.full((1 << 12,), -1, dtype=torch.int8, device=DEV).view(torch.uint8) if given else None
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms: the zeros come behind it
+            pages = kdn.Pages(table, lens, refs, 4, ws)
+        kdn.pages_reserve(pages, rows, 4, stream=other)  # three pages of two
+        torch.cuda.synchronize()
+        assert kdn.read_device_status(pages.workspace) == kdn.KDN_ERR_CAPACITY
+        k, v = (torch.zeros(2, 1, 4, 64, device=DEV) for _ in range(2))
+        kdn.pages_reserve(pages, rows[:2], 4, stream=other)
+        kdn.pages_reserve(pages, rows, 4, stream=other)  # refused
+        new = torch.ones(2, 1, 4, 64, device=DEV)
+        torch.cuda.synchronize()
+        kdn.pages_write(pages, rows[:2], new, new, k, v, stream=other)
+        torch.cuda.synchronize()
+        assert not k.any() and not v.any()
+        kdn.pages_free(pages, rows, stream=other)
+        torch.cuda.synchronize()
+
+
+def test_books_that_are_dropped_keep_their_memory_until_their_calls_have_ended():
+    """The workspace of books that die right after a call on another stream is not handed out again while the call waits."""
+    side = torch.cuda.Stream()
+    tables = [[_i32([[-1] * 4] * 3), _i32([0] * 3), _i32([0] * 2)] for _ in range(8)]
+    rows = _i32([0, 1, 2])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)  # about 20 ms
+    for t in tables:
+        kdn.pages_reserve(kdn.Pages(*t, 4), rows, 4, stream=side)  # refused: writes its status and marks
+    size = kdn.Pages(*tables[0], 4).workspace.numel()
+    mine = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(16)]
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in mine)
