@@ -673,7 +673,8 @@ int paged_step_splits(int dk, int dv, int in_dtype, int n, int H, int Hkv, long 
   // Two CTAs fit an SM.  One wave of parts of at least 128 tokens (below that a part is all start-up); for several
   // sequences, whose lengths differ, up to six waves of parts of at least 512 tokens, which even out.  Measured, 16
   // sequences of up to 16000 tokens on 4 heads, fp32: 111 us, one wave 154 us; 32 of up to 2000 on 8 heads, bf16: 40 us
-  // with parts of 512 tokens, 50 us with 285; 64 of up to 8192 on 8 heads: 164 us with six waves, 173 us with three.
+  // with parts of 512 tokens, 50 us with 285; 64 of up to 8192 on 8 heads: 164 us with six waves, 173 us with three (three
+  // CTAs per SM instead of two: 169 us against 165).
   const int hb = step_mma_supported(dk, dv, in_dtype) ? kMHB : head_block(G, in_dtype);
   const long long pairs = (long long)n * Hkv * ((G + hb - 1) / hb), slots = 2 * 148;
   const auto least = [](long long a, long long b) { return a < b ? a : b; };

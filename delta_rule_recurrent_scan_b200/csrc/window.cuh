@@ -67,9 +67,9 @@ __host__ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int windo
 // rows see few keys (the first rows of every sequence hold a third of the gradient's energy: 1.5 times the error of the
 // rounded result instead of 1.4), and there the walk is short.  So: up to 256 keys of the window, in tiles of T, and no more
 // than 128 sinks before them (a row behind those sees them all; backward of 2 sequences of 4096, 16 heads on 4, d 128,
-// window 64, 2048 sinks: 464 us, 571 with sweeps over all the sinks' tiles).  And, whatever o is, for queries from t0 on among which
-// one sees a single key: with its weight taken as 1 its delta is dP to the bit, and the gradient of a softmax over one key
-// the zero that it is.
+// window 64, 2048 sinks: 464 us, 571 with sweeps over all the sinks' tiles).  And, whatever o is, for queries from t0 on
+// among which one sees a single key: with its weight taken as 1 its delta is dP to the bit, and the gradient of a softmax
+// over one key the zero that it is.
 template <int T>
 __host__ __device__ __forceinline__ bool exact_delta(const WindowArgs& p, const KeyTiles& k, int t0, bool rounded) {
   const bool few = (k.hi - k.lo) * T <= 256 && (k.sinks == 0 || p.n_sink <= 128);

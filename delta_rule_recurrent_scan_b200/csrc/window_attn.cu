@@ -18,6 +18,8 @@
 // sinks): forward 108 us, backward 359 us; with one set of tiles 117 and 392 us; 4 x 4 values per thread with the rows
 // spread over the lanes (four wavefronts a read): 121 and 615 us; R = 16 (one CTA per SM, longer tail): 163 and 404 us;
 // three CTAs per SM (spills): 146 and 464 us.  Bound by latency: 8 to 16 warps an SM, the fp32 pipe about 40 % busy.
+// tf32 products in three parts were not taken: warp products run at 260 TFLOP/s of tf32, 87 after the split against 74 of
+// the fp32 pipe, with an accumulator that truncates.
 //
 // Rows past the sequence's end are staged as zeros, whatever memory holds.
 #include <cmath>

@@ -22,12 +22,16 @@
 // and some do not are compared.  Scaling, subtraction and sums take two values per instruction: with one warp of each
 // tile per scheduler the softmax is bound by the latency of its own instructions, not by a pipe.
 //
-// Measured, 4 sequences of 4096, 16 heads on 4 k/v heads, d = 128, window 1024, 4 sinks: 153 us (784 TFLOP/s of visible
+// Measured, 4 sequences of 4096, 16 heads on 4 k/v heads, d = 128, window 1024, 4 sinks: 151 us (800 TFLOP/s of visible
 // pairs; the tiles hold 1.25 times as many).  198 us with one CTA per work (start and end not overlapped, works in the
 // heads' order), 167 us with scalar instead of paired arithmetic, 158 us with descriptors built per product.  Without a
 // window, 16384 tokens: 1216 TFLOP/s.  A tile pair then takes 3750 cycles: products 2780 (q k^T reads two operands from
 // shared memory, 128 bytes a cycle, and runs at 0.6 of the rate of the other), the rest waits for a softmax to begin.
-// Moving 1/8 or 1/4 of the exponentials to the fp32 pipe (polynomial) made it 1 to 9 % slower; handing P over in halves 5 %.
+// Moving 1/8 or 1/4 of the exponentials to the fp32 pipe (polynomial) made it 1 to 9 % slower; handing P over in halves 5 %;
+// 384 threads with registers moved to the softmax warps (setmaxnreg) 25 to 60 %.  Steps of 32 columns for tiles that only
+// sinks make visible: no faster with sinks, 6 % slower without (the softmax warps' code got longer).
+//
+// A wait that gives up ends a role; the softmax warps then leave NaN in every row that they could not make (mark_rest).
 //
 // v rows behind a sequence's end are set to zero in shared memory (0 times whatever memory holds there would not be 0);
 // k rows behind it only reach hidden scores.

@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(256) window_rows_kernel(WindowArgs p, float2* 
         g[i] = c.x, g[i + 1] = c.y, g[i + 2] = c.z, g[i + 3] = c.w;
       }
       *reinterpret_cast<uint4*>(dO16 + at) = pack8_bf16(g, 1.f);  // an operand of two bf16 products
-      // delta from the same dO as dP: with the unrounded one P (dP - delta) would not add up to zero along a row (2.5 to
-      // 3.1 times the error of a rounded gradient where rows see few keys, 1.8 where they see many; 1.7 this way)
+      // delta from the same dO as dP: with the unrounded one P (dP - delta) would not add up to zero along a row.  Error of
+      // dq against rounding the exact one, windows of 2 to 16 keys: 1.9 to 2.4; this way 1.66 to 1.76 for every window
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = __bfloat162float(__float2bfloat16_rn(g[i]));
     }

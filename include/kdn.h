@@ -315,11 +315,11 @@ KDN_EXPORT kdn_status kdn_window_attn(const kdn_dims* dims, int kv_heads, const 
  *   dv_j = sum_t P_tj dO_t,  dq_t = scale sum_j dS_tj k_j,  dk_j = scale sum_t dS_tj q_t.
  * The scores are computed again, once for dq and once for dk and dv; every sum runs in a fixed order, so
  * gradients do not change from run to run.  On the tensor cores P and dS enter their products as bf16, and so does
- * dO, which is rounded to bf16 first where it comes as fp32.  Where rows see few keys and o is bf16 or comes from the
- * tensor cores, delta is made from P and dP instead of o.  Rows behind a sequence's last token are left as they were or set to zero (zero_rest),
- * in all three; lse has no upstream gradient.  A bounded wait that gives up (KDN_ERR_TIMEOUT) leaves NaN in every row of
- * dq, dk and dv that was not made because of it.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink,
- * 1) bytes. */
+ * dO, which is rounded to bf16 first where it comes as fp32 (errors of sqrt(2) and sqrt(3) times what rounding the exact
+ * gradient to bf16 costs).  Where rows see few keys and o is bf16 or comes from the tensor cores, delta is made from P and
+ * dP instead of o.  Rows behind a sequence's last token are left as they were or set to zero (zero_rest), in all three;
+ * lse has no upstream gradient.  A bounded wait that gives up (KDN_ERR_TIMEOUT) leaves NaN in every row of dq, dk and dv
+ * that was not made because of it.  workspace: kdn_window_workspace_bytes(dims, kv_heads, window, n_sink, 1) bytes. */
 KDN_EXPORT kdn_status kdn_window_attn_backward(const kdn_dims* dims, int kv_heads, const void* q, const void* k,
                                     const void* v, const int* lens, int zero_rest, int window, int n_sink, float scale,
                                     const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
