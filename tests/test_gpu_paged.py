@@ -667,3 +667,50 @@ def test_books_that_are_dropped_keep_their_memory_until_their_calls_have_ended()
     mine = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(16)]
     torch.cuda.synchronize()
     assert all(bool((x == 7).all()) for x in mine)
+
+
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("num,page,rows,most", [(12, 4, 6, 5), (9, 1, 5, 6), (30, 16, 8, 4)])
+def test_random_runs_keep_every_rows_tokens(num, page, rows, most, seed):
+    """Reservations, each followed by its write whether it was refused or not, forks and compactions with their copies,
+    freed rows: after every step each row reads back the tokens of a plain list."""
+    rng = random.Random(100 + seed)
+    pages = kdn.make_pages(num, page, rows, most)
+    k, v = (torch.zeros(num, 1, page, 16, device=DEV) for _ in range(2))
+    model, serial, refused = [[] for _ in range(rows)], 0, 0
+    for step in range(80):
+        op = rng.choice(["grow", "grow", "grow", "fork", "free", "compact"])
+        if op == "grow":
+            r = rng.sample(range(rows), rng.randint(1, rows))
+            c = [rng.randint(0, 2 * page) for _ in r]
+            T = max(1, *c)
+            new = torch.arange(serial, serial + len(r) * T, device=DEV, dtype=torch.float32).view(len(r), 1, T, 1)
+            new = new.expand(-1, -1, -1, 16).contiguous()
+            kdn.pages_reserve(pages, _i32(r), _i32(c))
+            kdn.pages_write(pages, _i32(r), new, -new, k, v, counts=_i32(c))
+            if kdn.read_device_status(pages.workspace) == kdn.KDN_OK:
+                for i, x in enumerate(r):
+                    model[x] += [serial + i * T + t for t in range(c[i])]
+            else:
+                refused += 1
+            serial += len(r) * T
+        elif op == "fork":
+            dst = [x for x in range(rows) if not model[x]][:2]
+            src = [rng.choice([x for x in range(rows) if x not in dst]) for _ in dst] if len(dst) < rows else []
+            kdn.pages_copy(kdn.pages_fork(pages, _i32(src), _i32(dst[:len(src)])), k, v)
+            if kdn.read_device_status(pages.workspace) == kdn.KDN_OK:
+                for a, b in zip(src, dst):
+                    model[b] = list(model[a])
+        elif op == "free":
+            r = rng.sample(range(rows), rng.randint(0, 2))
+            kdn.pages_free(pages, _i32(r))
+            for x in r:
+                model[x] = []
+        else:
+            kdn.pages_copy(kdn.pages_compact(pages), k, v)
+        assert pages.lens.tolist() == [len(x) for x in model]
+        table, kk, vv = pages.table.tolist(), k[:, 0, :, 0].tolist(), v[:, 0, :, 15].tolist()
+        for r, tokens in enumerate(model):
+            for j, x in enumerate(tokens):
+                assert kk[table[r][j // page]][j % page] == x and vv[table[r][j // page]][j % page] == -x, (step, op, r, j)
+    assert refused > 3
