@@ -668,7 +668,8 @@ class Pages:
             if self._fresh and self._home is not None and not torch.cuda.is_current_stream_capturing():
                 home = torch.cuda.ExternalStream(self._home, device=dev) if self._home else torch.cuda.default_stream(dev)
                 stream.wait_stream(home)
-        self.workspace.record_stream(stream)
+        if self.workspace.is_cuda:
+            self.workspace.record_stream(stream)
 
     def _c(self, dev=None):
         table, lens, refs = self.table, self.lens, self.refs

@@ -73,7 +73,7 @@ void run(const Case& c, int number) {
     for (char k : later.of) check(k == '.', "nothing behind the last round", number, cta);
     for (int r = (int)rounds - 1; r >= 0; --r) {
       Rows now = run.mark(r, cta);
-      std::vector<size_t> pairs;  // (head, tile) of what this round adds
+      std::vector<size_t> pairs;  // (head, tile) of what this work adds
       for (size_t e = 0; e < rows; ++e) {
         check(now.of[e] != '?', "whole rows, o and lse alike", number, cta);
         if (later.of[e] != '.') check(now.of[e] == later.of[e], "a later round's rows are marked too", number, cta);
@@ -85,7 +85,7 @@ void run(const Case& c, int number) {
       check(pairs.size() <= 2, "a round is one work: two tiles at most", number, cta);
       later = now;
     }
-    for (size_t e = 0; e < rows; ++e) {  // from round 0 on: every row of this CTA, with the value that belongs there
+    for (size_t e = 0; e < rows; ++e) {  // from the first work on: every row of this CTA, with the value that belongs there
       const int b = e / ((size_t)c.H * c.L), t = e % c.L, n = c.lens[b] < 0 ? 0 : c.lens[b] > c.L ? c.L : c.lens[b];
       if (later.of[e] != '.') check(later.of[e] == (t < n ? 'n' : '0'), "NaN in the sequence, zero behind it", number, t);
     }

@@ -714,3 +714,13 @@ def test_random_runs_keep_every_rows_tokens(num, page, rows, most, seed):
             for j, x in enumerate(tokens):
                 assert kk[table[r][j // page]][j % page] == x and vv[table[r][j // page]][j % page] == -x, (step, op, r, j)
     assert refused > 3
+
+
+def test_a_workspace_that_is_not_on_the_device_is_refused():
+    pages = kdn.make_pages(4, 16, 2, 2)
+    books = kdn.Pages(pages.table, pages.lens, pages.refs, 16, torch.zeros(1 << 12, dtype=torch.uint8))
+    with pytest.raises(kdn.KdnError, match="workspace"):
+        kdn.pages_free(books, _i32([0]))
+    short = kdn.Pages(pages.table, pages.lens, pages.refs, 16, torch.zeros(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(kdn.KdnError, match="workspace_bytes"):
+        kdn.pages_free(short, _i32([0]))
